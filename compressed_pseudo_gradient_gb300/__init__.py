@@ -17,6 +17,7 @@ from ._binding import (  # noqa: F401
     CALIB_SENDER_MOVES,
     CHUNK,
     FLAG_BAD_RECORD,
+    FLAG_BAD_TOKEN,
     FLAG_COPY_PENDING,
     FLAG_NONFINITE,
     FLAG_TIMEOUT,
@@ -42,4 +43,15 @@ from ._binding import (  # noqa: F401
     record_bytes,
     unpack,
     use_library,
+)
+from ._local import (  # noqa: F401
+    MAX_TOP,
+    NEWTON_SCHULZ,
+    TokenLogprobs,
+    embedding,
+    embedding_grad,
+    orthogonalize,
+    orthogonalize_workspace,
+    token_logprobs,
+    token_logprobs_grad,
 )

@@ -23,6 +23,7 @@ FLAG_NONFINITE = 1
 FLAG_BAD_RECORD = 2
 FLAG_TIMEOUT = 4
 FLAG_COPY_PENDING = 8
+FLAG_BAD_TOKEN = 32   # local-step operators: a token id outside the vocabulary
 SCALE_MAX_ABS = 0     # s = max |a| / 1.5 (the default)
 SCALE_MEAN_ABS = 1    # s = pairwise sum of the chosen |a| / k (codec variant)
 
@@ -120,10 +121,32 @@ def library():
         lib.spl_unpack.argtypes, lib.spl_unpack.restype = [vp, sz, vp, vp, vp], ci
         lib.spl_calib_moves.argtypes = [ci, ci, vp, vp, vp, vp, sz, vp, vp]
         lib.spl_calib_moves.restype = ci
+        _declare_local(lib)
         if hasattr(lib, "spl_debug_read"):   # the checked build
             lib.spl_debug_read.argtypes, lib.spl_debug_read.restype = [vp, ci], ci
         _lib = lib
         return lib
+
+
+def _declare_local(lib):
+    """Argument types of the local step's operators (include/spl_local.h)."""
+    vp, sz, ci, cf = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
+    lib.spl_token_logprobs.argtypes = [vp, ci, sz, sz, sz, vp, ci, cf, ci, vp, vp, vp, vp, vp, vp,
+                                       vp]
+    lib.spl_token_logprobs_grad.argtypes = [vp, ci, sz, sz, sz, vp, ci, cf, vp, vp, vp, vp, vp, sz,
+                                            vp, vp]
+    lib.spl_embedding.argtypes = [vp, ci, sz, vp, ci, sz, sz, sz, cf, vp, sz, vp, vp]
+    lib.spl_embedding_grad_workspace.argtypes = [sz, sz, sz]
+    lib.spl_embedding_grad.argtypes = [vp, ci, sz, vp, ci, sz, sz, sz, cf, ctypes.c_int64, ci, vp,
+                                       sz, vp, sz, vp, vp]
+    lib.spl_orthogonalize_workspace.argtypes = [sz, sz, sz]
+    lib.spl_orthogonalize.argtypes = [vp, ci, sz, sz, sz, sz, sz, vp, cf, ci, ci, vp, cf, vp, vp,
+                                      sz, vp, vp]
+    for fn in (lib.spl_token_logprobs, lib.spl_token_logprobs_grad, lib.spl_embedding,
+               lib.spl_embedding_grad, lib.spl_orthogonalize):
+        fn.restype = ci
+    for fn in (lib.spl_embedding_grad_workspace, lib.spl_orthogonalize_workspace):
+        fn.restype = sz
 
 
 DEBUG_WORDS = 16
@@ -144,7 +167,8 @@ def debug_words(reset: bool = False) -> dict:
 
 def flags_status(flags) -> int:
     """The status a device flags word stands for (spl_flags_status): 0 (ok), 4 (non-finite
-    accumulated value), 5 (rejected record) or 6 (a kernel stopped on a bounded wait).
+    accumulated value), 5 (rejected record), 6 (a kernel stopped on a bounded wait) or 7 (a token
+    id outside the vocabulary).
     ``flags`` is the 1-element int32 tensor the calls OR into, or its value; reading a tensor
     synchronises with its device."""
     if isinstance(flags, torch.Tensor):

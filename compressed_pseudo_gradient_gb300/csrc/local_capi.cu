@@ -1,0 +1,279 @@
+// C ABI of the local step's operators (declared in include/spl_local.h): argument checks on the
+// host, then stream-ordered kernel launches.  Nothing here allocates device memory or
+// synchronises.
+#include <cmath>
+
+#include "capi_util.h"
+#include "local_kernels.h"
+#include "spl_local.h"
+
+namespace {
+
+using spl::aligned;
+using spl::overlap;
+
+constexpr size_t kMaxDim = 0x7fffffff;
+constexpr size_t kMaxGrid = 0x7fffffff;
+
+bool known(spl_dtype dt) { return dt == SPL_F32 || dt == SPL_BF16; }
+size_t size_of(spl_dtype dt) { return dt == SPL_F32 ? 4 : 2; }
+bool id_width(int bits) { return bits == 32 || bits == 64; }
+cudaStream_t stream_of(spl_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// Bytes a [rows][cols] array with a row stride spans (rows, cols >= 1).
+size_t span(size_t rows, size_t cols, size_t stride, size_t size) {
+    return ((rows - 1) * stride + cols) * size;
+}
+
+struct Range {
+    const void* p;
+    size_t bytes;
+};
+
+bool any_overlap(Range out, const Range* others, int n) {
+    for (int i = 0; i < n; ++i)
+        if (overlap(out.p, out.bytes, others[i].p, others[i].bytes)) return true;
+    return false;
+}
+
+// Outputs overlap no input and no other output.
+bool disjoint(const Range* outs, int num_outs, const Range* ins, int num_ins) {
+    for (int i = 0; i < num_outs; ++i)
+        if (any_overlap(outs[i], ins, num_ins) || any_overlap(outs[i], outs, i)) return false;
+    return true;
+}
+
+// Sizes whose products stay far inside 64 bits.
+bool fits(size_t rows, size_t stride) { return rows <= kMaxDim && stride <= (size_t{1} << 40) / (rows > 0 ? rows : 1) * 64; }
+
+}  // namespace
+
+extern "C" {
+
+spl_status spl_token_logprobs(const void* logits, spl_dtype dtype, size_t rows, size_t vocab,
+                              size_t row_stride, const void* targets, int id_bits, float scale,
+                              int top, float* logp, float* lse, float* entropy, int64_t* top_ids,
+                              float* top_logp, uint32_t* d_flags, spl_stream_t stream) {
+    if (!known(dtype) || !id_width(id_bits)) return SPL_ERR_INVALID_ARG;
+    if (!(scale >= 1e-30f && scale <= 1e30f)) return SPL_ERR_INVALID_ARG;
+    if (vocab < 1 || vocab >= kMaxDim || row_stride < vocab || !fits(rows, row_stride))
+        return SPL_ERR_INVALID_ARG;
+    if (top < 0 || top > SPL_MAX_TOP || static_cast<size_t>(top) > vocab) return SPL_ERR_INVALID_ARG;
+    if (rows > kMaxGrid / 16) return SPL_ERR_INVALID_ARG;
+    if (rows == 0) return SPL_OK;
+    if (logits == nullptr || (targets != nullptr && logp == nullptr)) return SPL_ERR_INVALID_ARG;
+    if (top > 0 && (top_ids == nullptr || top_logp == nullptr)) return SPL_ERR_INVALID_ARG;
+    const size_t id_bytes = static_cast<size_t>(id_bits) / 8, k = static_cast<size_t>(top);
+    if (!aligned(logits, size_of(dtype)) || !aligned(targets, id_bytes) || !aligned(logp, 4) ||
+        !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(top_ids, 8) || !aligned(top_logp, 4) ||
+        !aligned(d_flags, 4))
+        return SPL_ERR_ALIGNMENT;
+    const Range ins[] = {{logits, span(rows, vocab, row_stride, size_of(dtype))},
+                         {targets, rows * id_bytes}};
+    const Range outs[] = {{targets != nullptr ? logp : nullptr, rows * 4}, {lse, rows * 4},
+                          {entropy, rows * 4}, {top > 0 ? top_ids : nullptr, rows * k * 8},
+                          {top > 0 ? top_logp : nullptr, rows * k * 4}, {d_flags, 4}};
+    if (!disjoint(outs, 6, ins, 2)) return SPL_ERR_INVALID_ARG;
+    spl::LogprobsArgs a = {};
+    a.logits = logits;
+    a.rows = static_cast<int64_t>(rows);
+    a.vocab = static_cast<int64_t>(vocab);
+    a.stride = static_cast<int64_t>(row_stride);
+    a.targets = {targets, id_bits == 64};
+    a.scale = scale;
+    a.top = top;
+    a.logp = logp;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    a.flags = d_flags;
+    return spl::cuda_status(spl::launch_logprobs(a, dtype == SPL_BF16, stream_of(stream)));
+}
+
+spl_status spl_token_logprobs_grad(const void* logits, spl_dtype dtype, size_t rows, size_t vocab,
+                                   size_t row_stride, const void* targets, int id_bits,
+                                   float scale, const float* lse, const float* d_logp,
+                                   const float* entropy, const float* d_entropy, void* d_logits,
+                                   size_t out_stride, uint32_t* d_flags, spl_stream_t stream) {
+    if (!known(dtype) || !id_width(id_bits)) return SPL_ERR_INVALID_ARG;
+    if (!(scale >= 1e-30f && scale <= 1e30f)) return SPL_ERR_INVALID_ARG;
+    if (vocab < 1 || vocab >= kMaxDim || row_stride < vocab || out_stride < vocab ||
+        !fits(rows, row_stride) || !fits(rows, out_stride))
+        return SPL_ERR_INVALID_ARG;
+    if (rows == 0) return SPL_OK;
+    // a launch has a CTA for every part of a row, at least 1,024 values each
+    if (rows > kMaxGrid / (vocab / 1024 + 2)) return SPL_ERR_INVALID_ARG;
+    if (logits == nullptr || lse == nullptr || d_logits == nullptr) return SPL_ERR_INVALID_ARG;
+    if ((targets == nullptr) != (d_logp == nullptr)) return SPL_ERR_INVALID_ARG;
+    if (d_entropy != nullptr && entropy == nullptr) return SPL_ERR_INVALID_ARG;
+    const size_t id_bytes = static_cast<size_t>(id_bits) / 8, size = size_of(dtype);
+    if (!aligned(logits, size) || !aligned(d_logits, size) || !aligned(targets, id_bytes) ||
+        !aligned(lse, 4) || !aligned(d_logp, 4) || !aligned(entropy, 4) || !aligned(d_entropy, 4) ||
+        !aligned(d_flags, 4))
+        return SPL_ERR_ALIGNMENT;
+    const bool in_place = d_logits == logits && out_stride == row_stride;
+    const Range ins[] = {{targets, rows * id_bytes}, {lse, rows * 4}, {d_logp, rows * 4},
+                         {d_entropy != nullptr ? entropy : nullptr, rows * 4}, {d_entropy, rows * 4},
+                         {in_place ? nullptr : logits, span(rows, vocab, row_stride, size)}};
+    const Range outs[] = {{d_logits, span(rows, vocab, out_stride, size)}, {d_flags, 4}};
+    if (!disjoint(outs, 2, ins, 6)) return SPL_ERR_INVALID_ARG;
+    spl::LogprobsGradArgs a = {};
+    a.logits = logits;
+    a.rows = static_cast<int64_t>(rows);
+    a.vocab = static_cast<int64_t>(vocab);
+    a.stride = static_cast<int64_t>(row_stride);
+    a.targets = {targets, id_bits == 64};
+    a.scale = scale;
+    a.lse = lse;
+    a.d_logp = d_logp;
+    a.entropy = entropy;
+    a.d_entropy = d_entropy;
+    a.out = d_logits;
+    a.out_stride = static_cast<int64_t>(out_stride);
+    a.flags = d_flags;
+    return spl::cuda_status(spl::launch_logprobs_grad(a, dtype == SPL_BF16, stream_of(stream)));
+}
+
+spl_status spl_embedding(const void* ids, int id_bits, size_t count, const void* table,
+                         spl_dtype dtype, size_t vocab, size_t width, size_t row_stride,
+                         float scale, void* out, size_t out_stride, uint32_t* d_flags,
+                         spl_stream_t stream) {
+    if (!known(dtype) || !id_width(id_bits) || !std::isfinite(scale)) return SPL_ERR_INVALID_ARG;
+    if (vocab < 1 || vocab >= kMaxDim || width < 1 || width > (size_t{1} << 30) ||
+        row_stride < width || out_stride < width || !fits(vocab, row_stride) ||
+        !fits(count, out_stride))
+        return SPL_ERR_INVALID_ARG;
+    if (count == 0) return SPL_OK;
+    if (count > kMaxGrid * size_t{512} / width) return SPL_ERR_INVALID_ARG;
+    if (ids == nullptr || table == nullptr || out == nullptr) return SPL_ERR_INVALID_ARG;
+    const size_t id_bytes = static_cast<size_t>(id_bits) / 8, size = size_of(dtype);
+    if (!aligned(ids, id_bytes) || !aligned(table, size) || !aligned(out, size) || !aligned(d_flags, 4))
+        return SPL_ERR_ALIGNMENT;
+    const Range ins[] = {{ids, count * id_bytes}, {table, span(vocab, width, row_stride, size)}};
+    const Range outs[] = {{out, span(count, width, out_stride, size)}, {d_flags, 4}};
+    if (!disjoint(outs, 2, ins, 2)) return SPL_ERR_INVALID_ARG;
+    spl::EmbeddingArgs a = {};
+    a.ids = {ids, id_bits == 64};
+    a.count = static_cast<int64_t>(count);
+    a.table = table;
+    a.vocab = static_cast<int64_t>(vocab);
+    a.width = static_cast<int64_t>(width);
+    a.stride = static_cast<int64_t>(row_stride);
+    a.scale = scale;
+    a.out = out;
+    a.out_stride = static_cast<int64_t>(out_stride);
+    a.flags = d_flags;
+    return spl::cuda_status(spl::launch_embedding(a, dtype == SPL_BF16, stream_of(stream)));
+}
+
+static bool grad_sizes(size_t count, size_t vocab, size_t width) {
+    return vocab >= 1 && vocab < kMaxDim && width >= 1 && width <= (size_t{1} << 30) &&
+           count <= kMaxDim && (count / 64 + 1) * (width / 256 + 1) + vocab <= kMaxGrid;
+}
+
+size_t spl_embedding_grad_workspace(size_t count, size_t vocab, size_t width) {
+    if (!grad_sizes(count, vocab, width)) return 0;
+    return spl::embedding_grad_workspace(static_cast<int64_t>(count), static_cast<int64_t>(vocab),
+                                         static_cast<int64_t>(width));
+}
+
+spl_status spl_embedding_grad(const void* ids, int id_bits, size_t count, const void* d_out,
+                              spl_dtype dtype, size_t width, size_t d_out_stride, size_t vocab,
+                              float scale, int64_t padding_id, int accumulate, float* d_table,
+                              size_t table_stride, void* workspace, size_t workspace_bytes,
+                              uint32_t* d_flags, spl_stream_t stream) {
+    if (!known(dtype) || !id_width(id_bits) || !std::isfinite(scale)) return SPL_ERR_INVALID_ARG;
+    if (!grad_sizes(count, vocab, width) || d_out_stride < width || table_stride < width ||
+        !fits(count, d_out_stride) || !fits(vocab, table_stride))
+        return SPL_ERR_INVALID_ARG;
+    if (count == 0 && accumulate) return SPL_OK;
+    if ((count > 0 && (ids == nullptr || d_out == nullptr)) || d_table == nullptr ||
+        workspace == nullptr)
+        return SPL_ERR_INVALID_ARG;
+    const size_t need = spl_embedding_grad_workspace(count, vocab, width);
+    if (workspace_bytes < need) return SPL_ERR_INVALID_ARG;
+    const size_t id_bytes = static_cast<size_t>(id_bits) / 8, size = size_of(dtype);
+    if (!aligned(ids, id_bytes) || !aligned(d_out, size) || !aligned(d_table, 4) ||
+        !aligned(workspace, 256) || !aligned(d_flags, 4))
+        return SPL_ERR_ALIGNMENT;
+    const Range ins[] = {{ids, count * id_bytes},
+                         {d_out, count > 0 ? span(count, width, d_out_stride, size) : 0}};
+    const Range outs[] = {{d_table, span(vocab, width, table_stride, 4)}, {workspace, need}, {d_flags, 4}};
+    if (!disjoint(outs, 3, ins, 2)) return SPL_ERR_INVALID_ARG;
+    spl::EmbeddingGradArgs a = {};
+    a.ids = {ids, id_bits == 64};
+    a.count = static_cast<int64_t>(count);
+    a.d_out = d_out;
+    a.d_out_stride = static_cast<int64_t>(d_out_stride);
+    a.vocab = static_cast<int64_t>(vocab);
+    a.width = static_cast<int64_t>(width);
+    a.scale = scale;
+    a.padding_id = padding_id;
+    a.accumulate = accumulate != 0;
+    a.d_table = d_table;
+    a.stride = static_cast<int64_t>(table_stride);
+    a.workspace = workspace;
+    a.flags = d_flags;
+    return spl::cuda_status(spl::launch_embedding_grad(a, dtype == SPL_BF16, stream_of(stream)));
+}
+
+static bool orth_sizes(size_t batch, size_t rows, size_t cols) {
+    constexpr size_t kSide = size_t{1} << 20;
+    return batch >= 1 && batch <= 65535 && rows >= 1 && rows <= kSide && cols >= 1 && cols <= kSide &&
+           // tile counts of all matrices stay in 31 bits
+           (rows / 128 + 1) * (cols / 128 + 1) <= kMaxGrid / batch;
+}
+
+size_t spl_orthogonalize_workspace(size_t batch, size_t rows, size_t cols) {
+    if (!orth_sizes(batch, rows, cols)) return 0;
+    return spl::orthogonalize_workspace(static_cast<int64_t>(batch), static_cast<int64_t>(rows),
+                                        static_cast<int64_t>(cols));
+}
+
+spl_status spl_orthogonalize(const void* update, spl_dtype dtype, size_t batch, size_t rows,
+                             size_t cols, size_t row_stride, size_t batch_stride,
+                             float* momentum, float mu, int nesterov, int steps,
+                             const float* coefficients, float eps, void* out, void* workspace,
+                             size_t workspace_bytes, uint32_t* d_flags, spl_stream_t stream) {
+    if (!known(dtype) || !orth_sizes(batch, rows, cols)) return SPL_ERR_INVALID_ARG;
+    if (row_stride < cols || !fits(rows, row_stride)) return SPL_ERR_INVALID_ARG;
+    const size_t one = (rows - 1) * row_stride + cols;   // values a matrix spans
+    if (batch > 1 && (batch_stride < one || !fits(batch, batch_stride))) return SPL_ERR_INVALID_ARG;
+    if (steps < 1 || steps > 32 || coefficients == nullptr) return SPL_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+        if (!(std::fabs(coefficients[i]) <= 8.0f)) return SPL_ERR_INVALID_ARG;
+    if (!std::isfinite(eps) || eps < 0.0f) return SPL_ERR_INVALID_ARG;
+    if (momentum != nullptr && !std::isfinite(mu)) return SPL_ERR_INVALID_ARG;
+    if (update == nullptr || out == nullptr || workspace == nullptr) return SPL_ERR_INVALID_ARG;
+    const size_t need = spl_orthogonalize_workspace(batch, rows, cols);
+    if (workspace_bytes < need) return SPL_ERR_INVALID_ARG;
+    const size_t size = size_of(dtype), values = batch * rows * cols;
+    if (!aligned(update, size) || !aligned(momentum, 4) || !aligned(out, 16) ||
+        !aligned(workspace, 256) || !aligned(d_flags, 4))
+        return SPL_ERR_ALIGNMENT;
+    const Range ins[] = {{update, ((batch - 1) * batch_stride + one) * size}};
+    const Range outs[] = {{momentum, values * 4}, {out, values * 2}, {workspace, need}, {d_flags, 4}};
+    if (!disjoint(outs, 4, ins, 1)) return SPL_ERR_INVALID_ARG;
+    // the products read their operands by bulk copies (TMA)
+    if (spl::memory_type(workspace) != cudaMemoryTypeDevice) return SPL_ERR_INVALID_ARG;
+    spl::OrthogonalizeArgs a = {};
+    a.update = update;
+    a.batch = static_cast<int64_t>(batch);
+    a.rows = static_cast<int64_t>(rows);
+    a.cols = static_cast<int64_t>(cols);
+    a.row_stride = static_cast<int64_t>(row_stride);
+    a.batch_stride = static_cast<int64_t>(batch_stride);
+    a.momentum = momentum;
+    a.mu = mu;
+    a.nesterov = nesterov != 0;
+    a.steps = steps;
+    for (int i = 0; i < 3; ++i) a.coef[i] = coefficients[i];
+    a.eps = eps;
+    a.out = static_cast<uint16_t*>(out);
+    a.workspace = workspace;
+    a.flags = d_flags;
+    return spl::cuda_status(spl::launch_orthogonalize(a, dtype == SPL_BF16, stream_of(stream)));
+}
+
+}  // extern "C"

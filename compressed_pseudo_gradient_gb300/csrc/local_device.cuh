@@ -1,0 +1,105 @@
+// Device-side helpers shared by the kernels of the local step's operators (spl_local.h).
+#pragma once
+
+#include "local_kernels.h"
+#include "spl_device.cuh"
+
+namespace spl {
+
+constexpr uint32_t kFlagBadToken = 32u;
+
+// Check sites of the checked build (after the codec's own, spl_device.cuh).
+enum LocalCheckSite : uint32_t {
+    kSiteLogits = 19, kSiteLogitsOut, kSiteTop, kSiteTable, kSiteRowsOut, kSiteSorted,
+    kSitePartials, kSiteOrthIn, kSiteOrthOut, kSiteOrthState, kSiteOrthEpilogue
+};
+
+constexpr float kLowest = -3.402823466e+38f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// max(a, b), NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+__device__ __forceinline__ int64_t token_at(const TokenIds& ids, int64_t i) {
+    return ids.wide ? static_cast<const int64_t*>(ids.data)[i]
+                    : static_cast<int64_t>(static_cast<const int32_t*>(ids.data)[i]);
+}
+
+// One 16-byte vector of a dense array: 4 fp32 or 8 bf16 values, widened to fp32.
+template <bool kBf16>
+struct Vec16 {
+    static constexpr int kN = kBf16 ? 8 : 4;
+    static constexpr int kBytes = kBf16 ? 2 : 4;
+
+    static __device__ __forceinline__ void unpack(const uint4& r, float (&x)[kN]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kBf16) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                x[i] = __uint_as_float(w[i]);
+            }
+        }
+    }
+
+    static __device__ __forceinline__ uint4 pack(const float (&x)[kN]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kBf16)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+            else
+                w[i] = __float_as_uint(x[i]);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+
+    // One value by its index, for rows and ends that are not 16-byte aligned.
+    static __device__ __forceinline__ float load1(const void* p, int64_t i) {
+        if constexpr (kBf16)
+            return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+        else
+            return static_cast<const float*>(p)[i];
+    }
+    static __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
+        if constexpr (kBf16) {
+            uint32_t w;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(0.0f), "f"(v));
+            static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w & 0xffffu);
+        } else {
+            static_cast<float*>(p)[i] = v;
+        }
+    }
+};
+
+// How a row of n values at `p` splits into 16-byte vectors: `head` values before the first
+// 16-byte boundary, `vecs` whole vectors, the rest after them.
+struct RowSplit {
+    int head;
+    int64_t vecs;
+};
+
+template <bool kBf16>
+__device__ __forceinline__ RowSplit split_row(const void* p, int64_t n) {
+    using V = Vec16<kBf16>;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) / V::kBytes;
+    RowSplit r;
+    r.head = off == 0 ? 0 : V::kN - off;
+    if (r.head > n) r.head = static_cast<int>(n);
+    r.vecs = (n - r.head) / V::kN;
+    return r;
+}
+
+}  // namespace spl

@@ -1,0 +1,102 @@
+// Host-side declarations of the launchers behind spl_local.h (internal header).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace spl {
+
+// Token ids of a call: 32- or 64-bit signed integers, or none.
+struct TokenIds {
+    const void* data;
+    bool wide;
+};
+
+constexpr int kMaxTop = 32;   // alternatives per row: one list entry per lane of a warp
+
+struct LogprobsArgs {
+    const void* logits;
+    int64_t rows, vocab, stride;
+    TokenIds targets;
+    float scale;
+    int top;
+    float* logp;
+    float* lse;
+    float* entropy;
+    int64_t* top_ids;
+    float* top_logp;
+    uint32_t* flags;
+};
+
+struct LogprobsGradArgs {
+    const void* logits;
+    int64_t rows, vocab, stride;
+    TokenIds targets;
+    float scale;
+    const float* lse;
+    const float* d_logp;      // or NULL
+    const float* entropy;     // with d_entropy only
+    const float* d_entropy;   // or NULL
+    void* out;
+    int64_t out_stride;
+    uint32_t* flags;
+};
+
+cudaError_t launch_logprobs(const LogprobsArgs& a, bool bf16, cudaStream_t stream);
+cudaError_t launch_logprobs_grad(const LogprobsGradArgs& a, bool bf16, cudaStream_t stream);
+
+struct EmbeddingArgs {
+    TokenIds ids;
+    int64_t count;
+    const void* table;
+    int64_t vocab, width, stride;
+    float scale;
+    void* out;
+    int64_t out_stride;
+    uint32_t* flags;
+};
+
+struct EmbeddingGradArgs {
+    TokenIds ids;
+    int64_t count;
+    const void* d_out;
+    int64_t d_out_stride;
+    int64_t vocab, width;
+    float scale;
+    int64_t padding_id;
+    bool accumulate;
+    float* d_table;
+    int64_t stride;
+    void* workspace;
+    uint32_t* flags;
+};
+
+cudaError_t launch_embedding(const EmbeddingArgs& a, bool bf16, cudaStream_t stream);
+size_t embedding_grad_workspace(int64_t count, int64_t vocab, int64_t width);
+cudaError_t launch_embedding_grad(const EmbeddingGradArgs& a, bool bf16, cudaStream_t stream);
+
+struct OrthogonalizeArgs {
+    const void* update;
+    int64_t batch, rows, cols, row_stride, batch_stride;
+    float* momentum;   // or NULL
+    float mu;
+    bool nesterov;
+    int steps;
+    float coef[3];
+    float eps;
+    uint16_t* out;
+    void* workspace;
+    uint32_t* flags;
+};
+
+size_t orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols);
+cudaError_t launch_orthogonalize(const OrthogonalizeArgs& a, bool bf16, cudaStream_t stream);
+
+#if SPL_CHECKED
+cudaError_t debug_read_logprobs(uint32_t* out, bool reset);
+cudaError_t debug_read_embedding(uint32_t* out, bool reset);
+cudaError_t debug_read_orthogonalize(uint32_t* out, bool reset);
+#endif
+
+}  // namespace spl

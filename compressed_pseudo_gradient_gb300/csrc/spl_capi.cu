@@ -4,6 +4,8 @@
 #include <cstring>
 #include <mutex>
 
+#include "capi_util.h"
+#include "local_kernels.h"
 #include "spl.h"
 #include "spl_calib.h"
 #include "spl_device.cuh"
@@ -16,25 +18,23 @@ namespace {
 
 thread_local int g_last_cuda_error = 0;
 
+constexpr size_t kMaxChunks = 0x7fffffff;   // chunk indices stay below 2^31
+
+using spl::aligned;
+using spl::cuda_status;
+using spl::memory_type;
+using spl::overlap;
+
+}  // namespace
+
+namespace spl {
+
 spl_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return SPL_OK;
     g_last_cuda_error = static_cast<int>(e);
     return SPL_ERR_CUDA;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Byte ranges [p, p + n) and [q, q + m) share a byte.
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-    if (p == nullptr || q == nullptr || n == 0 || m == 0) return false;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + m && b < a + n;
-}
-
-constexpr size_t kMaxChunks = 0x7fffffff;   // chunk indices stay below 2^31
-
-// CUDA memory type of a pointer (cudaMemoryTypeDevice, cudaMemoryTypeHost for pinned host
-// memory, ...), or -1 when the runtime cannot tell (the error is cleared).
 int memory_type(const void* p) {
     cudaPointerAttributes at;
     if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
@@ -43,10 +43,6 @@ int memory_type(const void* p) {
     }
     return static_cast<int>(at.type);
 }
-
-}  // namespace
-
-namespace spl {
 
 // Resident CTAs of a kernel on the current device (SMs x blocks per SM).  The device's SM
 // count is read once per device; the occupancy query is a host-side computation.
@@ -86,6 +82,7 @@ const char* spl_status_string(int status) {
         case SPL_ERR_NONFINITE: return "non-finite accumulated value";
         case SPL_ERR_BAD_PAYLOAD: return "rejected record";
         case SPL_ERR_TIMEOUT: return "kernel stopped on a bounded wait";
+        case SPL_ERR_BAD_TOKEN: return "token id out of range";
         default: return "unknown status";
     }
 }
@@ -93,6 +90,7 @@ const char* spl_status_string(int status) {
 spl_status spl_flags_status(uint32_t flags) {
     if (flags & (SPL_FLAG_TIMEOUT | SPL_FLAG_COPY_PENDING)) return SPL_ERR_TIMEOUT;
     if (flags & SPL_FLAG_BAD_RECORD) return SPL_ERR_BAD_PAYLOAD;
+    if (flags & SPL_FLAG_BAD_TOKEN) return SPL_ERR_BAD_TOKEN;
     if (flags & SPL_FLAG_NONFINITE) return SPL_ERR_NONFINITE;
     return SPL_OK;
 }
@@ -352,7 +350,8 @@ spl_status spl_debug_read(uint32_t* out, int reset) {
     if (out == nullptr) return SPL_ERR_INVALID_ARG;
     cudaError_t (*const readers[])(uint32_t*, bool) = {
         spl::debug_read_compress, spl::debug_read_compress_variants, spl::debug_read_decode,
-        spl::debug_read_decode_variants, spl::debug_read_pack};
+        spl::debug_read_decode_variants, spl::debug_read_pack, spl::debug_read_logprobs,
+        spl::debug_read_embedding, spl::debug_read_orthogonalize};
     for (int w = 0; w < spl::kDebugWords; ++w) out[w] = 0;
     for (auto rd : readers) {
         uint32_t d[spl::kDebugWords];

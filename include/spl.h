@@ -58,10 +58,11 @@ typedef enum {
     SPL_ERR_INVALID_ARG = 1, /* NULL pointer, bad size, non-finite beta/lr, overlap, bad dtype */
     SPL_ERR_ALIGNMENT = 2,   /* a pointer breaks the alignment rule above */
     SPL_ERR_CUDA = 3,        /* a CUDA call failed; see spl_last_cuda_error() */
-    /* the next three are only returned by spl_flags_status(), from a flags word read back */
+    /* the rest are only returned by spl_flags_status(), from a flags word read back */
     SPL_ERR_NONFINITE = 4,   /* some accumulated value a was NaN or infinite */
     SPL_ERR_BAD_PAYLOAD = 5, /* some record was rejected by the receiver's validation */
-    SPL_ERR_TIMEOUT = 6      /* a kernel stopped early on a bounded wait: outputs incomplete */
+    SPL_ERR_TIMEOUT = 6,     /* a kernel stopped early on a bounded wait: outputs incomplete */
+    SPL_ERR_BAD_TOKEN = 7    /* some token id was outside the vocabulary (spl_local.h) */
 } spl_status;
 
 typedef enum { SPL_F32 = 0, SPL_BF16 = 1 } spl_dtype;
@@ -80,13 +81,14 @@ enum {
     SPL_FLAG_NONFINITE = 1u,   /* sender: some a = beta * e + delta was not finite */
     SPL_FLAG_BAD_RECORD = 2u,  /* receiver: some record was rejected */
     SPL_FLAG_TIMEOUT = 4u,     /* a bounded wait for an asynchronous copy ran out */
-    SPL_FLAG_COPY_PENDING = 8u /* ... and so did the wait for that copy after stopping */
+    SPL_FLAG_COPY_PENDING = 8u, /* ... and so did the wait for that copy after stopping */
+    SPL_FLAG_BAD_TOKEN = 32u   /* some token id was outside the vocabulary (spl_local.h) */
 };
 
 /*
  * The status a flags word stands for, most severe first: SPL_ERR_TIMEOUT (SPL_FLAG_TIMEOUT or
- * SPL_FLAG_COPY_PENDING), SPL_ERR_BAD_PAYLOAD (SPL_FLAG_BAD_RECORD), SPL_ERR_NONFINITE
- * (SPL_FLAG_NONFINITE), else SPL_OK.  A host-side helper: `flags` is the value read back.
+ * SPL_FLAG_COPY_PENDING), SPL_ERR_BAD_PAYLOAD (SPL_FLAG_BAD_RECORD), SPL_ERR_BAD_TOKEN
+ * (SPL_FLAG_BAD_TOKEN), SPL_ERR_NONFINITE (SPL_FLAG_NONFINITE), else SPL_OK.  A host-side helper: `flags` is the value read back.
  */
 spl_status spl_flags_status(uint32_t flags);
 

@@ -1,0 +1,147 @@
+/*
+ * spl_local.h: operators of a peer's local step, next to the codec of spl.h: what makes a
+ * pseudo-gradient (the matrices' orthogonalised momentum, the embedding table's lookup and
+ * gradient, the token log-probabilities' gradient) and what scores a received one (the token
+ * log-probabilities before and after it is applied).
+ *
+ * The conventions are those of spl.h: device pointers owned by the caller, work enqueued on
+ * `stream` and never waited for, nothing allocated and nothing kept between calls, argument
+ * errors returned synchronously, device-side conditions OR-ed into *d_flags (NULL: not reported).
+ * A call that needs scratch memory takes a device workspace (256-byte aligned) of at least the
+ * size its _workspace function gives, free for other use once the stream has passed the call.
+ * Dense arrays are fp32 or bf16 (spl_dtype) and need only the alignment of their type; 16-byte
+ * aligned rows run faster.  Strides count values.  Token ids are 64- or 32-bit signed integers
+ * (id_bits).  All sums are held in fp32 or more, and a call gives the same bits every time: no
+ * result depends on the order of atomics.
+ */
+#ifndef SPL_LOCAL_H_
+#define SPL_LOCAL_H_
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "spl.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+enum { SPL_MAX_TOP = 32 }; /* most alternatives spl_token_logprobs returns per row */
+
+/*
+ * Log-probabilities of given tokens under rows of logits, with the rows' entropy and most
+ * probable alternatives.  With z = scale * logits[r], for each of `rows` rows:
+ *
+ *   lse[r]     = log sum_j exp(z_j)
+ *   logp[r]    = z_t - lse[r], t = targets[r];  0 where t < 0 (a position outside the loss);
+ *                NaN, and SPL_FLAG_BAD_TOKEN, where t >= vocab
+ *   entropy[r] = - sum_j p_j log p_j, p_j = exp(z_j - lse[r])   (0 log 0 = 0)
+ *   top_ids[r], top_logp[r] = the `top` tokens of largest logit, descending, equal logits by
+ *                ascending id, and their log-probabilities
+ *
+ * A logit of -inf is a token ruled out (probability 0).  A row of nothing else gives
+ * lse = logp = top_logp = -inf and entropy 0.  A row with a NaN or +inf gives NaN throughout
+ * and SPL_FLAG_NONFINITE (a NaN ranks above every number in top_ids).
+ *
+ * logits:  [rows][vocab], row_stride >= vocab; vocab >= 1, below 2^31
+ * targets: [rows] or NULL (then logp is not written and may be NULL)
+ * scale:   positive, 1e-30 .. 1e30 (an inverse temperature)
+ * top:     0 .. SPL_MAX_TOP, at most vocab; 0: top_ids and top_logp may be NULL
+ * logp, lse, entropy: [rows] fp32; lse and entropy may be NULL
+ * top_ids, top_logp:  [rows][top] int64 and fp32
+ * Outputs must not overlap the logits, the targets or each other.
+ */
+spl_status spl_token_logprobs(const void* logits, spl_dtype dtype, size_t rows, size_t vocab,
+                              size_t row_stride, const void* targets, int id_bits, float scale,
+                              int top, float* logp, float* lse, float* entropy, int64_t* top_ids,
+                              float* top_logp, uint32_t* d_flags, spl_stream_t stream);
+
+/*
+ * Gradient of the above with respect to the logits, from the forward call's lse (and entropy):
+ *
+ *   d_logits[r][j] = scale * (d_logp[r] (1[j = t] - p_j) - d_entropy[r] p_j (z_j - lse[r] + entropy[r]))
+ *
+ * The d_logp term is left out where t < 0 (or t >= vocab: SPL_FLAG_BAD_TOKEN), and for the whole
+ * call when targets and d_logp are NULL; the entropy term when d_entropy is NULL (entropy is
+ * then not read).  A row with lse = -inf has gradient 0.
+ *
+ * d_logits: [rows][vocab] of the logits' dtype, out_stride >= vocab; may be the logits
+ *           themselves (same pointer and stride), otherwise no array may overlap it
+ */
+spl_status spl_token_logprobs_grad(const void* logits, spl_dtype dtype, size_t rows, size_t vocab,
+                                   size_t row_stride, const void* targets, int id_bits,
+                                   float scale, const float* lse, const float* d_logp,
+                                   const float* entropy, const float* d_entropy, void* d_logits,
+                                   size_t out_stride, uint32_t* d_flags, spl_stream_t stream);
+
+/*
+ * Embedding lookup: out[i] = scale * table[ids[i]], computed in fp32 and rounded once.  An id
+ * outside 0 .. vocab - 1 gives a row of zeros and SPL_FLAG_BAD_TOKEN.
+ *
+ * table: [vocab][width], row_stride >= width;  out: [count][width] of the same dtype,
+ * out_stride >= width, overlapping neither the table nor the ids.  scale is finite.
+ */
+spl_status spl_embedding(const void* ids, int id_bits, size_t count, const void* table,
+                         spl_dtype dtype, size_t vocab, size_t width, size_t row_stride,
+                         float scale, void* out, size_t out_stride, uint32_t* d_flags,
+                         spl_stream_t stream);
+
+/* Bytes of workspace spl_embedding_grad needs (0 for sizes it does not accept). */
+size_t spl_embedding_grad_workspace(size_t count, size_t vocab, size_t width);
+
+/*
+ * Gradient of the lookup with respect to the table:
+ *
+ *   d_table[v] (+)= scale * (sum of d_out[i] over the i with ids[i] = v, fp32)
+ *
+ * accumulate 0: every row of d_table is written (zeros where no token has its id);
+ * accumulate 1: the sums are added to d_table, rows without tokens are left alone.
+ * Tokens with ids[i] = padding_id take no part (-1: no such id).  Tokens outside the table take
+ * no part either and set SPL_FLAG_BAD_TOKEN.  Tokens of one id are added in ascending i within
+ * groups of at most 64, groups in order.
+ *
+ * d_out: [count][width] of `dtype`, d_out_stride >= width;  d_table: [vocab][width] fp32,
+ * table_stride >= width.  count, vocab and width are below 2^31.
+ */
+spl_status spl_embedding_grad(const void* ids, int id_bits, size_t count, const void* d_out,
+                              spl_dtype dtype, size_t width, size_t d_out_stride, size_t vocab,
+                              float scale, int64_t padding_id, int accumulate, float* d_table,
+                              size_t table_stride, void* workspace, size_t workspace_bytes,
+                              uint32_t* d_flags, spl_stream_t stream);
+
+/* Bytes of workspace spl_orthogonalize needs (0 for sizes it does not accept). */
+size_t spl_orthogonalize_workspace(size_t batch, size_t rows, size_t cols);
+
+/*
+ * Orthogonalised update of `batch` matrices (rows x cols) by Newton-Schulz products, with the
+ * momentum step of a matrix optimiser in front:
+ *
+ *   u = G;  with momentum: M <- mu M + G (in place), u = G + mu M (nesterov) or u = M
+ *   X = u / (|u|_F + eps), transposed where rows > cols
+ *   `steps` times:  A = X X^T,  X <- c0 X + (c1 A + c2 A A) X
+ *   out = X (transposed back) in bf16
+ *
+ * Products have fp16 operands and fp32 sums, and X is carried in 22 bits between steps: with the
+ * usual coefficients (3.4445, -4.7750, 2.0315) and 5 steps the result is within 2e-3 of the
+ * formula's (2-norm, before its rounding to bf16), whatever the spread of the singular values.
+ * A matrix of zeros gives zeros.  One whose norm is not finite gives NaN and
+ * SPL_FLAG_NONFINITE; entries should lie within about 1e-18 .. 1e18 (their squares are summed).
+ *
+ * update:   [batch][rows][cols] of `dtype`; row_stride >= cols, batch_stride between matrices
+ * momentum: [batch][rows][cols] fp32, contiguous, or NULL (mu and nesterov are then ignored)
+ * steps:    1 .. 32;  coefficients: 3 finite values of at most 8 in size
+ * out:      [batch][rows][cols] bf16, contiguous
+ * batch, rows, cols: >= 1; batch <= 65535, rows and cols <= 2^20
+ * SPL_FLAG_TIMEOUT as for the codec calls, if a bulk copy does not land in bounded time.
+ */
+spl_status spl_orthogonalize(const void* update, spl_dtype dtype, size_t batch, size_t rows,
+                             size_t cols, size_t row_stride, size_t batch_stride,
+                             float* momentum, float mu, int nesterov, int steps,
+                             const float* coefficients, float eps, void* out, void* workspace,
+                             size_t workspace_bytes, uint32_t* d_flags, spl_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SPL_LOCAL_H_ */
