@@ -221,8 +221,10 @@ spl_status spl_embedding_grad(const void* ids, int id_bits, size_t count, const 
 static bool orth_sizes(size_t batch, size_t rows, size_t cols) {
     constexpr size_t kSide = size_t{1} << 20;
     return batch >= 1 && batch <= 65535 && rows >= 1 && rows <= kSide && cols >= 1 && cols <= kSide &&
-           // tile counts of all matrices stay in 31 bits
-           (rows / 128 + 1) * (cols / 128 + 1) <= kMaxGrid / batch;
+           // tile counts of all matrices stay in 31 bits, and one product well under the second
+           // that a wait may take
+           (rows / 128 + 1) * (cols / 128 + 1) * batch <= (size_t{1} << 24) &&
+           batch * rows * cols <= (size_t{1} << 46) / (rows < cols ? rows : cols);
 }
 
 size_t spl_orthogonalize_workspace(size_t batch, size_t rows, size_t cols) {
@@ -255,8 +257,10 @@ spl_status spl_orthogonalize(const void* update, spl_dtype dtype, size_t batch, 
     const Range ins[] = {{update, ((batch - 1) * batch_stride + one) * size}};
     const Range outs[] = {{momentum, values * 4}, {out, values * 2}, {workspace, need}, {d_flags, 4}};
     if (!disjoint(outs, 4, ins, 1)) return SPL_ERR_INVALID_ARG;
-    // the products read their operands by bulk copies (TMA)
-    if (spl::memory_type(workspace) != cudaMemoryTypeDevice) return SPL_ERR_INVALID_ARG;
+    // the products' operands and results move by bulk copies (TMA)
+    if (spl::memory_type(workspace) != cudaMemoryTypeDevice ||
+        spl::memory_type(out) != cudaMemoryTypeDevice)
+        return SPL_ERR_INVALID_ARG;
     spl::OrthogonalizeArgs a = {};
     a.update = update;
     a.batch = static_cast<int64_t>(batch);

@@ -22,6 +22,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <mutex>
 
 #include "local_device.cuh"
 #include "local_kernels.h"
@@ -36,6 +37,7 @@ constexpr float kLoScale = 2048.0f;      // of the state's low plane
 // ---- momentum, norm, state ------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
 constexpr int kMaxPartials = 512;   // sums of squares per matrix
+constexpr int kMaxPhases = 160;     // of the run kernel below
 
 struct PrepArgs {
     const void* update;
@@ -49,6 +51,7 @@ struct PrepArgs {
     __half* hi;         // [batch][m][ld]
     __half* lo;
     int64_t ld, plane;  // plane = m * ld
+    uint32_t* arrived;  // the run kernel's phase counters, cleared here
     uint32_t* flags;
 };
 
@@ -58,28 +61,81 @@ __device__ __forceinline__ float step_value(float g, float m, const PrepArgs& p)
     return p.nesterov ? __fmaf_rn(p.mu, m, g) : m;
 }
 
+// A matrix as a flat range of units (16-byte vectors of the update where its rows allow, single
+// values otherwise): a CTA takes kPrepUnits per thread at a time, so that short rows share a CTA.
+constexpr int kPrepUnits = 4;
+
+template <bool kBf16, bool kVec>
+struct PrepUnit {
+    static constexpr int kN = kVec ? Vec16<kBf16>::kN : 1;
+    float x[kN];
+
+    __device__ __forceinline__ void load(const PrepArgs& p, int64_t b, int64_t r, int64_t u) {
+        const unsigned char* row = static_cast<const unsigned char*>(p.update) +
+                                   (b * p.batch_stride + r * p.row_stride) * Vec16<kBf16>::kBytes;
+        if constexpr (kVec) Vec16<kBf16>::unpack(reinterpret_cast<const uint4*>(row)[u], x);
+        else x[0] = Vec16<kBf16>::load1(row, u);
+    }
+    __device__ __forceinline__ void load_momentum(const float* m) {
+        if constexpr (kVec) {
+#pragma unroll
+            for (int i = 0; i < kN; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(m + i);
+                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+            }
+        } else {
+            x[0] = *m;
+        }
+    }
+    __device__ __forceinline__ void store_momentum(float* m) const {
+        if constexpr (kVec) {
+#pragma unroll
+            for (int i = 0; i < kN; i += 4)
+                *reinterpret_cast<float4*>(m + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        } else {
+            *m = x[0];
+        }
+    }
+};
+
 // The momentum step and each CTA's share of |u|^2.
-template <bool kBf16>
+template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kPrepThreads) k_orth_norm(const __grid_constant__ PrepArgs p) {
-    using V = Vec16<kBf16>;
+    using U = PrepUnit<kBf16, kVec>;
     __shared__ double s_sum[kPrepThreads / 32];
     const int64_t b = blockIdx.y;
+    if (blockIdx.x == 0 && b == 0 && threadIdx.x < kMaxPhases) p.arrived[threadIdx.x] = 0;
+    const uint32_t per_row = static_cast<uint32_t>(p.cols / U::kN);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPrepThreads * kPrepUnits);
     double total = 0.0;
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        const unsigned char* row = static_cast<const unsigned char*>(p.update) +
-                                   (b * p.batch_stride + r * p.row_stride) * V::kBytes;
-        float* mom = p.momentum == nullptr ? nullptr : p.momentum + (b * p.rows + r) * p.cols;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kPrepThreads * kPrepUnits);
+         first < p.rows * per_row; first += step) {
+        const int64_t row0 = first / per_row;
+        const uint32_t rem0 = static_cast<uint32_t>(first - row0 * per_row);
+        U g[kPrepUnits], m[kPrepUnits];
+        int64_t at[kPrepUnits];
+#pragma unroll
+        for (int k = 0; k < kPrepUnits; ++k) {
+            const uint32_t i = rem0 + k * kPrepThreads + threadIdx.x;
+            const int64_t r = row0 + i / per_row;
+            at[k] = -1;
+            if (r >= p.rows || !SPL_CHECK(r < p.rows, kSiteOrthIn, r)) continue;
+            const uint32_t u = i % per_row;
+            g[k].load(p, b, r, u);
+            at[k] = (b * p.rows + r) * p.cols + static_cast<int64_t>(u) * U::kN;
+            if (p.momentum != nullptr) m[k].load_momentum(p.momentum + at[k]);
+        }
         float sum = 0.0f;
-        for (int64_t c = threadIdx.x; c < p.cols; c += kPrepThreads) {
-            if (!SPL_CHECK(c < p.cols, kSiteOrthIn, c)) continue;
-            const float g = V::load1(row, c);
-            float m = 0.0f;
-            if (mom != nullptr) {
-                m = __fmaf_rn(p.mu, mom[c], g);
-                mom[c] = m;
+#pragma unroll
+        for (int k = 0; k < kPrepUnits; ++k) {
+            if (at[k] < 0) continue;
+#pragma unroll
+            for (int i = 0; i < U::kN; ++i) {
+                if (p.momentum != nullptr) m[k].x[i] = __fmaf_rn(p.mu, m[k].x[i], g[k].x[i]);
+                const float u = step_value(g[k].x[i], m[k].x[i], p);
+                sum = __fmaf_rn(u, u, sum);
             }
-            const float u = step_value(g, m, p);
-            sum = __fmaf_rn(u, u, sum);
+            if (p.momentum != nullptr) m[k].store_momentum(p.momentum + at[k]);
         }
         total += static_cast<double>(sum);
     }
@@ -93,28 +149,16 @@ __global__ void __launch_bounds__(kPrepThreads) k_orth_norm(const __grid_constan
     }
 }
 
-__device__ __forceinline__ void store_state(__half* hi, __half* lo, int64_t at, float x) {
-    const __half h = __float2half_rn(x);
-    hi[at] = h;
-    lo[at] = __float2half_rn(__fmul_rn(__fsub_rn(x, __half2float(h)), kLoScale));
-}
-
-// X = u / (|u| + eps) in the state's format, through a 32 x 32 tile in shared memory when the
-// matrix is tall.
-template <bool kBf16, bool kTall>
-__global__ void __launch_bounds__(kPrepThreads) k_orth_state(const __grid_constant__ PrepArgs p) {
-    using V = Vec16<kBf16>;
+// x_scale / (|u| + eps) of matrix b, the same in every thread of the CTA.
+__device__ __forceinline__ float state_factor(const PrepArgs& p, int64_t b) {
     __shared__ double s_sum[kPrepThreads / 32];
     __shared__ float s_factor;
-    __shared__ float s_tile[32][33];
-    const int64_t b = blockIdx.z;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     double total = 0.0;
     for (int i = threadIdx.x; i < p.num_partials; i += kPrepThreads)
         total += p.partials[b * kMaxPartials + i];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(kAll, total, off);
-    if (lane == 0) s_sum[warp] = total;
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = total;
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < kPrepThreads / 32; ++w) total += s_sum[w];
@@ -126,77 +170,196 @@ __global__ void __launch_bounds__(kPrepThreads) k_orth_state(const __grid_consta
         }
     }
     __syncthreads();
-    const float f = s_factor;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 32, c0 = static_cast<int64_t>(blockIdx.x) * 32;
-    __half* hi = p.hi + b * p.plane;
-    __half* lo = p.lo + b * p.plane;
+    return s_factor;
+}
+
+__device__ __forceinline__ void split_state(float x, __half& hi, __half& lo) {
+    hi = __float2half_rn(x);
+    lo = __float2half_rn(__fmul_rn(__fsub_rn(x, __half2float(hi)), kLoScale));
+}
+
+// kN consecutive values of the state's two planes.
+template <int kN>
+__device__ __forceinline__ void store_state(const PrepArgs& p, int64_t at, const float* x) {
+    __half h[kN], l[kN];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + warp + 8 * i, c = c0 + lane;
-        if (r >= p.rows || c >= p.cols || !SPL_CHECK(r < p.rows, kSiteOrthIn, r)) continue;
-        const float g = V::load1(static_cast<const unsigned char*>(p.update) +
-                                     (b * p.batch_stride + r * p.row_stride) * V::kBytes, c);
-        const float m = p.momentum == nullptr ? 0.0f : p.momentum[(b * p.rows + r) * p.cols + c];
-        const float x = __fmul_rn(step_value(g, m, p), f);
-        if constexpr (kTall)
-            s_tile[warp + 8 * i][lane] = x;
-        else
-            store_state(hi, lo, r * p.ld + c, x);
+    for (int i = 0; i < kN; ++i) split_state(x[i], h[i], l[i]);
+    if constexpr (kN == 8) {
+        *reinterpret_cast<uint4*>(p.hi + at) = *reinterpret_cast<const uint4*>(h);
+        *reinterpret_cast<uint4*>(p.lo + at) = *reinterpret_cast<const uint4*>(l);
+    } else if constexpr (kN == 4) {
+        *reinterpret_cast<uint2*>(p.hi + at) = *reinterpret_cast<const uint2*>(h);
+        *reinterpret_cast<uint2*>(p.lo + at) = *reinterpret_cast<const uint2*>(l);
+    } else {
+        p.hi[at] = h[0];
+        p.lo[at] = l[0];
     }
-    if constexpr (kTall) {
-        __syncthreads();
+}
+
+// X = u / (|u| + eps) in the state's format.
+template <bool kBf16, bool kVec>
+__global__ void __launch_bounds__(kPrepThreads) k_orth_state(const __grid_constant__ PrepArgs p) {
+    using U = PrepUnit<kBf16, kVec>;
+    const int64_t b = blockIdx.y;
+    const float f = state_factor(p, b);
+    const uint32_t per_row = static_cast<uint32_t>(p.cols / U::kN);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPrepThreads * kPrepUnits);
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kPrepThreads * kPrepUnits);
+         first < p.rows * per_row; first += step) {
+        const int64_t row0 = first / per_row;
+        const uint32_t rem0 = static_cast<uint32_t>(first - row0 * per_row);
+        U g[kPrepUnits], m[kPrepUnits];
+        int64_t at[kPrepUnits];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = r0 + lane, c = c0 + warp + 8 * i;   // the state's column and row
-            if (r < p.rows && c < p.cols && SPL_CHECK(r < p.ld, kSiteOrthState, r))
-                store_state(hi, lo, c * p.ld + r, s_tile[lane][warp + 8 * i]);
+        for (int k = 0; k < kPrepUnits; ++k) {
+            const uint32_t i = rem0 + k * kPrepThreads + threadIdx.x;
+            const int64_t r = row0 + i / per_row;
+            at[k] = -1;
+            if (r >= p.rows || !SPL_CHECK(r < p.rows, kSiteOrthIn, r)) continue;
+            const uint32_t u = i % per_row;
+            g[k].load(p, b, r, u);
+            if (p.momentum != nullptr)
+                m[k].load_momentum(p.momentum + (b * p.rows + r) * p.cols + static_cast<int64_t>(u) * U::kN);
+            at[k] = b * p.plane + r * p.ld + static_cast<int64_t>(u) * U::kN;
+        }
+#pragma unroll
+        for (int k = 0; k < kPrepUnits; ++k) {
+            if (at[k] < 0) continue;
+#pragma unroll
+            for (int i = 0; i < U::kN; ++i) g[k].x[i] = __fmul_rn(step_value(g[k].x[i], m[k].x[i], p), f);
+            store_state<U::kN>(p, at[k], g[k].x);
         }
     }
 }
 
+// The same for a tall matrix, whose state is its transpose: 64 x 64 tiles through shared memory.
+template <bool kBf16, bool kVec>
+__global__ void __launch_bounds__(kPrepThreads) k_orth_state_tall(const __grid_constant__ PrepArgs p) {
+    using U = PrepUnit<kBf16, kVec>;
+    constexpr int kAcross = 64 / U::kN, kDown = kPrepThreads / kAcross;
+    __shared__ float s_tile[64][65];
+    const int64_t b = blockIdx.z;
+    const float f = state_factor(p, b);
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64, c0 = static_cast<int64_t>(blockIdx.y) * 64;
+    const int uc = threadIdx.x % kAcross, ur = threadIdx.x / kAcross;
+#pragma unroll
+    for (int k = 0; k < 64 / kDown; ++k) {
+        const int64_t r = r0 + ur + k * kDown, c = c0 + uc * U::kN;
+        if (r >= p.rows || c >= p.cols || !SPL_CHECK(r < p.rows, kSiteOrthIn, r)) continue;
+        U g, m;
+        g.load(p, b, r, c / U::kN);
+        if (p.momentum != nullptr) m.load_momentum(p.momentum + (b * p.rows + r) * p.cols + c);
+#pragma unroll
+        for (int i = 0; i < U::kN; ++i)
+            s_tile[ur + k * kDown][uc * U::kN + i] = __fmul_rn(step_value(g.x[i], m.x[i], p), f);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {   // 8 of the tile's rows per thread: the state's columns
+        const int c = (threadIdx.x >> 3) + 32 * k, r = (threadIdx.x & 7) * 8;
+        if (c0 + c >= p.cols || r0 + r >= p.rows) continue;
+        // columns up to the row pitch, a multiple of 8, are this buffer's own
+        if (!SPL_CHECK(r0 + r + 8 <= p.ld, kSiteOrthState, r0 + r)) continue;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = s_tile[r + i][c];
+        store_state<8>(p, b * p.plane + (c0 + c) * p.ld + r0 + r, x);
+    }
+}
+
+template <bool kBf16, bool kVec>
+cudaError_t launch_prep(PrepArgs p, int64_t batch, bool tall, int sms, cudaStream_t stream) {
+    const int64_t per_cta = static_cast<int64_t>(kPrepThreads) * kPrepUnits;
+    const int64_t ctas = (p.rows * (p.cols / PrepUnit<kBf16, kVec>::kN) + per_cta - 1) / per_cta;
+    p.num_partials = static_cast<int>(ctas < kMaxPartials ? ctas : kMaxPartials);
+    const unsigned b = static_cast<unsigned>(batch);
+    k_orth_norm<kBf16, kVec><<<dim3(static_cast<unsigned>(p.num_partials), b), kPrepThreads, 0, stream>>>(p);
+    if (tall) {
+        const dim3 grid(static_cast<unsigned>((p.rows + 63) / 64), static_cast<unsigned>((p.cols + 63) / 64), b);
+        k_orth_state_tall<kBf16, kVec><<<grid, kPrepThreads, 0, stream>>>(p);
+    } else {
+        const int64_t most = 16 * static_cast<int64_t>(sms);   // a few waves, then loop
+        k_orth_state<kBf16, kVec><<<dim3(static_cast<unsigned>(ctas < most ? ctas : most), b), kPrepThreads, 0,
+                                    stream>>>(p);
+    }
+    return cudaGetLastError();
+}
+
 // ---- the products ---------------------------------------------------------------------------
-enum Product { kGram = 0, kPoly = 1, kUpdate = 2, kLast = 3 };   // kLast: the update that ends it
+// All products of a call run in one persistent cooperative kernel, as a list of phases with a
+// barrier over the grid between them.  A phase computes D = A B^T (B's rows along K) or D = A B
+// (B's rows along N) tile by tile, and for each tile
+//
+//   value = f_acc * accumulator + f1 * source1 + f2 * source2
+//
+// written as one fp16 plane (a symmetric product also to its mirrored place), as the state's two
+// planes, or as bf16 (in place or transposed).  Per CTA: one thread issues the operands' TMA loads
+// into a ring of stages, one the MMAs, one the TMA loads of the sources' 128 x 64 slabs, four
+// warps turn accumulators into results in the slabs' shared memory, and one thread issues the TMA
+// stores that take them from there.  Two accumulators in tensor memory let a tile's MMAs run under the previous tile's
+// epilogue.
+//
+// kPair = 2: two CTAs form a 256 x 256 tile (cta_group::2: each loads its 128 rows of A and half
+// of B, and holds 128 rows of the result), which halves the operand traffic into shared memory;
+// kPair = 1: 128 x 128 tiles, four times as many, for problems too small to fill the GPU.
+//
+// Every wait is bounded; on a timeout a role leaves its loops after waiting (bounded) for what it
+// has in flight, the others follow by their own timeouts, and the flags word says so.
+constexpr int kBlock = 128;                  // rows of a CTA's part of a tile
+constexpr int kTileK = 64;
+constexpr int kSlab = 64;                    // columns of an epilogue slab
+constexpr int kStages = 4;
+constexpr int kOperandBytes = kBlock * kTileK * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kPlaneBytes = kBlock * kSlab * 2;
+constexpr int kSlabBytes = 3 * kPlaneBytes;  // two source planes, replaced by results; a mirror
+constexpr int kSlabs = 2;
+constexpr int kRunThreads = 256;
+constexpr int kRunSmem = kStages * kStageBytes + kSlabs * kSlabBytes + 1024;
+constexpr int kMaxMatrices = 12;
+constexpr uint8_t kNone = 255;
 
-constexpr int kTileM = 128, kTileK = 64;
-constexpr int kGemmThreads = 192;          // four epilogue warps, one for TMA, one for the MMAs
-constexpr int kEpiCols = 64;               // columns of a tile per epilogue step
-constexpr int kEpiPitch = kEpiCols + 1;    // floats; odd: columns and rows both read without conflicts
+enum ResultKind : uint8_t { kPlane, kState, kBf16, kBf16Transposed, kPartial };
 
-template <int kTileN>
-struct GemmShape {
-    static constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2;
-    static constexpr int kStage = kBytesA + kBytesB;
-    static constexpr int kEpilogue = 4 * 32 * kEpiPitch * 4;
-    static constexpr int kStages = (227 * 1024 - 2048 - kEpilogue) / kStage;
-    static constexpr int kSmem = kStages * kStage + kEpilogue + 1024 + 512;
-    static constexpr int kTmemCols = 2 * kTileN;   // two accumulators
+struct Phase {
+    uint8_t a, b, src1, src2, dst, dst_lo;   // matrices, or kNone
+    uint8_t result;                          // ResultKind
+    bool b_along_n, sym;
+    bool reduce;      // sum the previous phase's partial accumulators instead of a product
+    uint8_t splits;   // parts of K (results are kPartial unless 1); of a reduce: partials per tile
+    int n, k;         // columns of the result, length of the product
+    float f_acc, f1, f2;
 };
 
-struct GemmArgs {
-    int m, n, k;                 // of the product
-    int tiles_m, tiles_n, tiles; // tiles per matrix
-    int total_tiles;
-    int batch;
-    float fa, fb;                // value = fa * source + fb * accumulator
-    const __half* src_hi;        // kPoly: A; kUpdate, kLast: X
-    const __half* src_lo;
-    int64_t src_ld, src_plane;
-    __half* dst_hi;
-    __half* dst_lo;
-    int64_t dst_ld, dst_plane;
-    uint16_t* out;               // kLast
-    int64_t out_ld, out_plane;
-    bool tall;                   // kLast: out holds X^T
+struct OrthRun {
+    CUtensorMap wide[kMaxMatrices];     // boxes of 64 columns x 128 rows
+    CUtensorMap narrow[kMaxMatrices];   // 64 x 64
+    Phase phases[kMaxPhases];
+    int num_phases, m, batch;
+    float* partials;      // [unit][column / 4][row][4] of kPartial phases
+    uint32_t* arrived;    // a counter per phase, zero at launch
     uint32_t* flags;
 };
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                            uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-        : "memory");
+// kCtas = 2: the copy is one of a pair's, counted on the barrier of the pair's first CTA.
+template <int kCtas>
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                         uint32_t bar) {
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];"
+            ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];"
+            ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(src)) : "memory");
 }
 
 // Shared-memory operand descriptor, 128-byte swizzle (rows of 64 fp16, groups of 8 rows 1,024
@@ -208,20 +371,45 @@ __device__ __forceinline__ uint64_t operand_desc(const void* p, uint32_t lead) {
            (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+template <int kCtas>
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
-        : "memory");
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
 }
 
+// Arrives on the barrier (of both CTAs of a pair) once the MMAs issued so far are done.
+template <int kCtas>
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 ::"r"(smem_addr(bar)) : "memory");
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+            ::"r"(smem_addr(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     ::"r"(smem_addr(bar)) : "memory");
 }
 
-__device__ __forceinline__ void tmem_load_32(uint32_t addr, uint32_t (&v)[32]) {
+// Address of a shared variable in the pair's first CTA.
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(p)));
+    return a;
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_load_32(uint32_t addr, uint32_t* v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -234,45 +422,85 @@ __device__ __forceinline__ void tmem_load_32(uint32_t addr, uint32_t (&v)[32]) {
         : "r"(addr));
 }
 
-struct TileAt {
-    int b, i, j;   // matrix, tile row, tile column
+__device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// Waits until `count` CTAs have arrived on a phase's counter; bounded.
+__device__ __forceinline__ bool grid_wait(const uint32_t* counter, uint32_t count) {
+    uint32_t v;
+    uint64_t t0 = 0;
+    for (;;) {
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+        if (v >= count) return true;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) return false;
+    }
+}
+
+// ---- units of work --------------------------------------------------------------------------
+struct UnitAt {
+    int b, i, j;       // matrix, tile row, tile column
+    int k0, k1;        // blocks of K
+    int slab0, slab1;  // slabs of the tile
+    int tile;          // index of the tile over all matrices
 };
 
-// Tiles of a symmetric product: tile row i (128 rows) has the columns' tiles that reach its last
-// row's diagonal.  kRatio = kTileN / kTileM tile rows share a count.
-template <bool kSym, int kTileN>
-__device__ __forceinline__ TileAt tile_at(const GemmArgs& g, int t) {
-    TileAt at;
-    at.b = t / g.tiles;
-    int r = t - at.b * g.tiles;
-    if constexpr (kSym) {
-        constexpr int kRatio = kTileN / kTileM;
-        // the first p groups of kRatio tile rows hold kRatio p (p + 1) / 2 tiles
-        const float q = static_cast<float>(2 * r) / kRatio;
-        int p = static_cast<int>((sqrtf(1.0f + 4.0f * q) - 1.0f) * 0.5f);
-        while (kRatio * p * (p + 1) / 2 > r) --p;
-        while (kRatio * (p + 1) * (p + 2) / 2 <= r) ++p;
-        r -= kRatio * p * (p + 1) / 2;
-        at.i = p * kRatio + r / (p + 1);
-        at.j = r % (p + 1);
-    } else {
-        at.i = r % g.tiles_m;
-        at.j = r / g.tiles_m;
+template <int kPair>
+struct Tiling {
+    static constexpr int kTile = kBlock * kPair;   // rows and columns of a tile
+    static constexpr int kTileSlabs = kTile / kSlab;
+
+    static __host__ __device__ __forceinline__ int tiles(int m, const Phase& p) {
+        const int tm = (m + kTile - 1) / kTile, tn = (p.n + kTile - 1) / kTile;
+        return p.sym ? tm * (tm + 1) / 2 : tm * tn;
     }
-    return at;
-}
+    // A reduce phase deals out single slabs, a split product parts of K.
+    static __host__ __device__ __forceinline__ int units(int m, int batch, const Phase& p) {
+        return tiles(m, p) * batch * (p.reduce ? kTileSlabs : p.splits);
+    }
+    static __device__ __forceinline__ UnitAt at(int m, const Phase& p, int u) {
+        UnitAt a;
+        const int per = p.reduce ? kTileSlabs : p.splits;
+        a.tile = u / per;
+        const int part = u - a.tile * per;
+        const int tiles_b = tiles(m, p);
+        a.b = a.tile / tiles_b;
+        const int r = a.tile - a.b * tiles_b;
+        if (p.sym) {   // tile row i starts at i (i + 1) / 2
+            int i = static_cast<int>((sqrtf(1.0f + 8.0f * static_cast<float>(r)) - 1.0f) * 0.5f);
+            while (i * (i + 1) / 2 > r) --i;
+            while ((i + 1) * (i + 2) / 2 <= r) ++i;
+            a.i = i;
+            a.j = r - i * (i + 1) / 2;
+        } else {       // groups of 8 tile rows, so that the tiles in flight share both operands
+            const int tm = (m + kTile - 1) / kTile, tn = (p.n + kTile - 1) / kTile;
+            const int g = r / (8 * tn), h = min(8, tm - 8 * g), q = r - g * 8 * tn;
+            a.i = 8 * g + q % h;
+            a.j = q / h;
+        }
+        const int blocks = (p.k + kTileK - 1) / kTileK;
+        a.k0 = p.reduce ? 0 : blocks * part / p.splits;
+        a.k1 = p.reduce ? 0 : blocks * (part + 1) / p.splits;
+        a.slab0 = p.reduce ? part : 0;
+        a.slab1 = p.reduce ? part + 1 : kTileSlabs;
+        return a;
+    }
+};
+
+// Byte offset of 16-byte chunk c of row r in a 128-byte-swizzled plane.
+__device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 __device__ __forceinline__ void unpack_half8(const uint4& r, float (&x)[8]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __half2 h = *reinterpret_cast<const __half2*>(&w[i]);
-        x[2 * i] = __low2float(h);
-        x[2 * i + 1] = __high2float(h);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
     }
 }
 
-__device__ __forceinline__ uint4 pack_half8(const float (&x)[8]) {
+__device__ __forceinline__ uint4 pack_half8(const float* x) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -282,297 +510,470 @@ __device__ __forceinline__ uint4 pack_half8(const float (&x)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint16_t half_bits(float x) {
-    const __half h = __float2half_rn(x);
-    return *reinterpret_cast<const uint16_t*>(&h);
+// A row's 16-byte chunk (8 results of 16 bits) of the transposed plane.  Neighbouring lanes hold
+// neighbouring rows: the even lane takes the pair of rows of the chunk's first four columns, the
+// odd lane of the last four, in words of two rows.  Columns four apart differ in the swizzle's
+// bit 2, so the two lanes' words fall into different halves of the banks.
+__device__ __forceinline__ void store_transposed(unsigned char* plane, int row, int chunk, const uint4& w) {
+    const int r = row & 62;   // 64 rows per block; the pair's first row
+    const bool odd = (row & 1) != 0;
+    unsigned char* block = plane + (row >> 6) * (kSlab * 128);
+    const uint32_t give0 = odd ? w.x : w.z, give1 = odd ? w.y : w.w;
+    const uint32_t keep0 = odd ? w.z : w.x, keep1 = odd ? w.w : w.y;
+    const uint32_t got0 = __shfl_xor_sync(kAll, give0, 1), got1 = __shfl_xor_sync(kAll, give1, 1);
+    const uint32_t even_row[2] = {odd ? got0 : keep0, odd ? got1 : keep1};
+    const uint32_t odd_row[2] = {odd ? keep0 : got0, odd ? keep1 : got1};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int col = chunk * 8 + (odd ? 4 : 0) + i;
+        const uint32_t out = __byte_perm(even_row[i >> 1], odd_row[i >> 1], (i & 1) ? 0x7632 : 0x5410);
+        *reinterpret_cast<uint32_t*>(block + swizzled(col, r >> 3) + (r & 7) * 2) = out;
+    }
 }
 
-__device__ __forceinline__ uint16_t bf16_bits(float x) {
-    uint32_t w;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(0.0f), "f"(x));
-    return static_cast<uint16_t>(w);
-}
-
-// One epilogue step of a warp: 32 rows from row0, kEpiCols columns from col0, accumulators in buf.
-// Direct places take 8 columns per lane, 4 rows at a time; transposed ones 8 rows per lane, 8
-// columns at a time.
-template <int kMode>
-__device__ __forceinline__ void epilogue_step(const GemmArgs& g, float* buf, int b, int row0,
-                                              int col0, int lane) {
-    constexpr bool kSym = kMode == kGram || kMode == kPoly;
-    // values in place: buf becomes fa * source + fb * accumulator
-#pragma unroll 2
-    for (int it = 0; it < 8; ++it) {
-        const int lr = it * 4 + (lane >> 3), lc = (lane & 7) * 8;
-        const int r = row0 + lr, c = col0 + lc;
-        if (r >= g.m || c >= g.n || (kSym && c > r)) continue;
-        float v[8];
-        float* at = buf + lr * kEpiPitch + lc;
+// A thread's row of a slab: accumulators v to results in the slab's planes.
+template <int kSources, ResultKind kResult, bool kMirror>
+__device__ __forceinline__ void finish_row(unsigned char* slab, int row, float (&v)[kSlab], float f_acc,
+                                           float f1, float f2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(g.fb, at[i]);
-        if constexpr (kMode != kGram) {
-            float s[8];
-            const int64_t from = b * g.src_plane + r * g.src_ld + c;
-            if (!SPL_CHECK(c + 8 <= g.src_ld, kSiteOrthState, c)) continue;
-            unpack_half8(*reinterpret_cast<const uint4*>(g.src_hi + from), s);
-            if constexpr (kMode == kUpdate || kMode == kLast) {
-                float l[8];
-                unpack_half8(*reinterpret_cast<const uint4*>(g.src_lo + from), l);
+    for (int c = 0; c < kSlab / 8; ++c) {
+        float* x = v + 8 * c;
+        uint4* p0 = reinterpret_cast<uint4*>(slab + swizzled(row, c));
+        uint4* p1 = reinterpret_cast<uint4*>(slab + kPlaneBytes + swizzled(row, c));
+        float y[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[i] = __fmaf_rn(l[i], 1.0f / kLoScale, s[i]);
-            }
+        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], f_acc);
+        if constexpr (kSources == 2) {
+            unpack_half8(*p1, y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmaf_rn(g.fa, s[i], v[i]);
+            for (int i = 0; i < 8; ++i) x[i] = __fmaf_rn(f2, y[i], x[i]);
         }
-        if constexpr (kMode == kLast) {
-            if (!g.tall) {
-                uint16_t* to = g.out + b * g.out_plane + static_cast<int64_t>(r) * g.out_ld + c;
-                if (!SPL_CHECK(r < g.m, kSiteOrthOut, r)) continue;
-                if (c + 8 <= g.n && (g.out_ld & 7) == 0) {
-                    *reinterpret_cast<uint4*>(to) = Vec16<true>::pack(v);
-                } else {
+        if constexpr (kSources >= 1) {
+            unpack_half8(*p0, y);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c + i < g.n) to[i] = bf16_bits(v[i]);
-                }
-            }
+            for (int i = 0; i < 8; ++i) x[i] = __fmaf_rn(f1, y[i], x[i]);
+        }
+        uint4 w;
+        if constexpr (kResult == kBf16 || kResult == kBf16Transposed) {
+            const float z[8] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+            w = Vec16<true>::pack(z);
         } else {
-            __half* to = g.dst_hi + b * g.dst_plane + r * g.dst_ld + c;
-            if (!SPL_CHECK(c + 8 <= g.dst_ld, kSiteOrthState, c)) continue;
-            if (!kSym || c + 7 <= r) {   // columns up to the row pitch are this buffer's own
-                const uint4 h = pack_half8(v);
-                *reinterpret_cast<uint4*>(to) = h;
-                if constexpr (kMode == kUpdate) {
-                    float back[8], l[8];
-                    unpack_half8(h, back);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        l[i] = __fmul_rn(__fsub_rn(v[i], back[i]), kLoScale);
-                    *reinterpret_cast<uint4*>(g.dst_lo + b * g.dst_plane + r * g.dst_ld + c) = pack_half8(l);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (c + i <= r) reinterpret_cast<uint16_t*>(to)[i] = half_bits(v[i]);
-            }
+            w = pack_half8(x);
         }
-        if (kSym || (kMode == kLast && g.tall)) {
+        if constexpr (kResult != kBf16Transposed) *p0 = w;
+        if constexpr (kResult == kState) {
+            unpack_half8(w, y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) at[i] = v[i];
+            for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(__fsub_rn(x[i], y[i]), kLoScale);
+            *p1 = pack_half8(y);
         }
+        if constexpr (kMirror || kResult == kBf16Transposed)
+            store_transposed(slab + 2 * kPlaneBytes, row, c, w);
     }
-    if (!(kSym || (kMode == kLast && g.tall))) return;
-    __syncwarp();
-#pragma unroll 2
-    for (int it = 0; it < 8; ++it) {
-        const int lc = it * 8 + (lane >> 2), lr = (lane & 3) * 8;
-        const int r = row0 + lr, c = col0 + lc;
-        if (r >= g.m || c >= g.n || (kSym && r + 7 <= c)) continue;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = buf[(lr + i) * kEpiPitch + lc];
-        if constexpr (kMode == kLast) {
-            uint16_t* to = g.out + b * g.out_plane + static_cast<int64_t>(c) * g.out_ld + r;
-            if (!SPL_CHECK(c < g.n, kSiteOrthOut, c)) continue;
-            if (r + 8 <= g.m && (g.out_ld & 7) == 0) {
-                *reinterpret_cast<uint4*>(to) = Vec16<true>::pack(v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (r + i < g.m) to[i] = bf16_bits(v[i]);
-            }
-        } else {   // strictly above the diagonal; the diagonal is written in place above
-            __half* to = g.dst_hi + b * g.dst_plane + c * g.dst_ld + r;
-            if (!SPL_CHECK(r + 8 <= g.dst_ld, kSiteOrthState, r)) continue;
-            if (r > c && r + 8 <= g.m) {
-                *reinterpret_cast<uint4*>(to) = pack_half8(v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (r + i > c && r + i < g.m) reinterpret_cast<uint16_t*>(to)[i] = half_bits(v[i]);
-            }
-        }
-    }
-    __syncwarp();
 }
 
-// D = A B^T (B's rows run along K) for kGram and kPoly, D = A B (B's rows run along N) for the
-// updates, tile by tile: one thread issues TMA loads into a ring of stages, one issues the MMAs,
-// four warps turn finished accumulators into results while the next tile's MMAs run (two
-// accumulators in tensor memory).  Every wait is bounded; on a timeout all roles leave their
-// loops, wait (bounded) for what is in flight, and the flags word says so.
-template <int kMode, int kTileN>
-__global__ void __launch_bounds__(kGemmThreads, 1)
-k_orth_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-               const __grid_constant__ GemmArgs g) {
-    using S = GemmShape<kTileN>;
-    constexpr bool kSym = kMode == kGram || kMode == kPoly;
-    constexpr bool kBRowsAlongN = !kSym;
+template <int kPair>
+__global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_constant__ OrthRun run) {
+    using T = Tiling<kPair>;
+    constexpr int kAccCols = T::kTile;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* stages = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    float* epi = reinterpret_cast<float*>(stages + S::kStages * S::kStage);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(stages + S::kStages * S::kStage + S::kEpilogue);
-    uint64_t* full = bars;
-    uint64_t* empty = bars + S::kStages;
-    uint64_t* acc_full = bars + 2 * S::kStages;
-    uint64_t* acc_empty = acc_full + 2;
-    uint64_t* drain = acc_full + 4;
-    __shared__ uint32_t s_tmem, s_late;
+    unsigned char* slabs = stages + kStages * kStageBytes;
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2],
+        src_full[kSlabs], src_empty[kSlabs], done[kSlabs], drain;
+    __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int k_blocks = (g.k + kTileK - 1) / kTileK;
+    const int rank = kPair == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
+    const int group = blockIdx.x / kPair, groups = gridDim.x / kPair;
 
     if (tid == 0) {
-        for (int s = 0; s < S::kStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&acc_full[s], 1);
-            mbar_init(&acc_empty[s], 4);
+            mbar_init(&acc_empty[s], 4 * kPair);
         }
-        mbar_init(drain, 1);
-        s_late = 0;
+        for (int s = 0; s < kSlabs; ++s) {
+            mbar_init(&src_full[s], 1);
+            mbar_init(&src_empty[s], 1);
+            mbar_init(&done[s], 4);
+        }
+        mbar_init(&drain, 1);
         fence_async_smem();
     }
     if (warp == 5) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(smem_addr(&s_tmem)), "n"(S::kTmemCols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if constexpr (kPair == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                         ::"r"(smem_addr(&s_tmem)), "n"(2 * kAccCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                         ::"r"(smem_addr(&s_tmem)), "n"(2 * kAccCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
+    if constexpr (kPair == 2) {   // the other CTA's barriers are set up too
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
+    bool late = false;
 
     if (warp == 4) {
-        if (lane == 0) {
-            int stage = 0;
+        if (lane == 0) {   // operands
+            int stage = 0, used = 0;
             uint32_t phase = 0;
-            int used = 0;   // stages ever filled, up to kStages
-            bool late = false;
-            for (int t = blockIdx.x; t < g.total_tiles && !late; t += gridDim.x) {
-                const TileAt at = tile_at<kSym, kTileN>(g, t);
-                for (int kb = 0; kb < k_blocks; ++kb) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1u)) {
-                        late = true;
-                        break;
-                    }
-                    unsigned char* a = stages + stage * S::kStage;
-                    unsigned char* b = a + S::kBytesA;
-                    mbar_expect_tx(&full[stage], S::kStage);
-                    tma_load_3d(a, &map_a, kb * kTileK, at.i * kTileM, at.b, &full[stage]);
-                    if constexpr (kBRowsAlongN) {
-#pragma unroll
-                        for (int q = 0; q < kTileN / 64; ++q)
-                            tma_load_3d(b + q * 64 * kTileK * 2, &map_b, at.j * kTileN + q * 64,
-                                        kb * kTileK, at.b, &full[stage]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < kTileN / 128; ++q)
-                            tma_load_3d(b + q * 128 * kTileK * 2, &map_b, kb * kTileK,
-                                        at.j * kTileN + q * 128, at.b, &full[stage]);
-                    }
-                    if (used < S::kStages) ++used;
-                    if (++stage == S::kStages) {
-                        stage = 0;
-                        phase ^= 1u;
+            for (int ph = 0; ph < run.num_phases && !late; ++ph) {
+                const Phase p = run.phases[ph];
+                if (p.reduce) continue;
+                if (ph > 0 && !grid_wait(run.arrived + ph - 1, gridDim.x)) {
+                    late = true;
+                    break;
+                }
+                fence_async_all();
+                const int units = T::units(run.m, run.batch, p);
+                for (int u = group; u < units && !late; u += groups) {
+                    const UnitAt at = T::at(run.m, p, u);
+                    for (int kb = at.k0; kb < at.k1; ++kb) {
+                        if (!mbar_wait(&empty[stage], phase ^ 1u)) {
+                            late = true;
+                            break;
+                        }
+                        unsigned char* a = stages + stage * kStageBytes;
+                        unsigned char* b = a + kOperandBytes;
+                        const uint32_t bar = kPair == 2 ? leader_addr(&full[stage]) : smem_addr(&full[stage]);
+                        if (rank == 0) mbar_expect_tx(&full[stage], kPair * kStageBytes);
+                        const int row = at.i * T::kTile + rank * kBlock, col = at.j * T::kTile + rank * kBlock;
+                        tma_load<kPair>(a, &run.wide[p.a], kb * kTileK, row, at.b, bar);
+                        if (p.b_along_n) {
+                            tma_load<kPair>(b, &run.narrow[p.b], col, kb * kTileK, at.b, bar);
+                            tma_load<kPair>(b + kOperandBytes / 2, &run.narrow[p.b], col + 64, kb * kTileK, at.b, bar);
+                        } else {
+                            tma_load<kPair>(b, &run.wide[p.b], kb * kTileK, col, at.b, bar);
+                        }
+                        if (used < kStages) ++used;
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
                 }
             }
-            if (late) {   // the copies still in flight must land before the CTA leaves
+            if (late) {
+                // the copies still in flight must land before the CTA leaves; a pair's are all
+                // counted in its first CTA, and the second waits for that one before it exits
                 bool pending = false;
-                for (int q = 0; q < used; ++q) {
-                    const int s = (stage + S::kStages - 1 - q) % S::kStages;
-                    const uint32_t ph = s < stage ? phase : phase ^ 1u;
-                    pending |= !mbar_wait(&full[s], ph);
+                for (int q = 0; q < used && rank == 0; ++q) {
+                    const int s = (stage + kStages - 1 - q) % kStages;
+                    pending |= !mbar_wait(&full[s], s < stage ? phase : phase ^ 1u);
                 }
-                if (g.flags != nullptr)
-                    atomicOr(g.flags, kFlagTimeout | (pending ? kFlagCopyPending : 0u));
+                if (run.flags != nullptr)
+                    atomicOr(run.flags, kFlagTimeout | (pending ? kFlagCopyPending : 0u));
             }
         }
         __syncwarp();
     } else if (warp == 5) {
-        if (lane == 0) {
-            // fp32 accumulators, fp16 operands, B transposed where its rows run along N
-            constexpr uint32_t idesc = (1u << 4) | ((kBRowsAlongN ? 1u : 0u) << 16) |
-                                       (static_cast<uint32_t>(kTileN / 8) << 17) |
-                                       (static_cast<uint32_t>(kTileM / 16) << 24);
+        if (lane == 0 && rank == 0) {   // products
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            bool late = false;
-            for (int t = blockIdx.x; t < g.total_tiles && !late; t += gridDim.x) {
-                if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u)) {
-                    late = true;
-                    break;
-                }
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (int kb = 0; kb < k_blocks; ++kb) {
-                    if (!mbar_wait(&full[stage], phase)) {
+            for (int ph = 0; ph < run.num_phases && !late; ++ph) {
+                const Phase p = run.phases[ph];
+                if (p.reduce) continue;
+                // fp32 accumulators, fp16 operands, B transposed where its rows run along N
+                const uint32_t idesc = (1u << 4) | ((p.b_along_n ? 1u : 0u) << 16) |
+                                       (static_cast<uint32_t>(T::kTile / 8) << 17) |
+                                       (static_cast<uint32_t>(T::kTile / 16) << 24);
+                const uint32_t lead = p.b_along_n ? kOperandBytes / 2 : 16;
+                const uint32_t b_step = p.b_along_n ? 128 : 2;   // 16 of K: 16 rows, or 32 bytes
+                const int units = T::units(run.m, run.batch, p);
+                for (int u = group; u < units && !late; u += groups) {
+                    const UnitAt at = T::at(run.m, p, u);
+                    if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u)) {
                         late = true;
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const unsigned char* a = stages + stage * S::kStage;
-                    const uint64_t da = operand_desc(a, 16);
-                    const uint64_t db = operand_desc(a + S::kBytesA, kBRowsAlongN ? 64 * kTileK * 2 : 16);
+                    for (int kb = at.k0; kb < at.k1; ++kb) {
+                        if (!mbar_wait(&full[stage], phase)) {
+                            late = true;
+                            break;
+                        }
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const unsigned char* a = stages + stage * kStageBytes;
+                        const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperandBytes, lead);
 #pragma unroll
-                    for (int k = 0; k < kTileK / 16; ++k)   // 16 values of K: 32 bytes, or 16 rows
-                        mma_f16(tmem + acc * kTileN, da + k * 2, db + k * (kBRowsAlongN ? 128 : 2),
-                                idesc, kb > 0 || k > 0);
-                    mma_commit(&empty[stage]);
-                    if (++stage == S::kStages) {
-                        stage = 0;
+                        for (int k = 0; k < kTileK / 16; ++k)
+                            mma_f16<kPair>(tmem + acc * kAccCols, da + k * 2, db + k * b_step, idesc,
+                                           kb > at.k0 || k > 0);
+                        mma_commit<kPair>(&empty[stage]);
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (late) break;
+                    mma_commit<kPair>(&acc_full[acc]);
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
+            }
+            if (late) {
+                mma_commit<kPair>(&drain);
+                mbar_wait(&drain, 0);
+                if (run.flags != nullptr) atomicOr(run.flags, kFlagTimeout);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        if (lane == 0) {   // sources
+            int buf = 0, used = 0;
+            uint32_t phase = 0;
+            for (int ph = 0; ph < run.num_phases && !late; ++ph) {
+                const Phase p = run.phases[ph];
+                if (ph > 0 && !grid_wait(run.arrived + ph - 1, gridDim.x)) {
+                    late = true;
+                    break;
+                }
+                fence_async_all();
+                const int units = T::units(run.m, run.batch, p);
+                for (int u = group; u < units && !late; u += groups) {
+                    const UnitAt at = T::at(run.m, p, u);
+                    const int row = at.i * T::kTile + rank * kBlock;
+                    if (row >= run.m) continue;
+                    for (int s = at.slab0; s < at.slab1; ++s) {
+                        const int col = at.j * T::kTile + s * kSlab;
+                        if (col >= p.n) break;
+                        if (!mbar_wait(&src_empty[buf], phase ^ 1u)) {
+                            late = true;
+                            break;
+                        }
+                        unsigned char* slab = slabs + buf * kSlabBytes;
+                        const uint32_t bar = smem_addr(&src_full[buf]);
+                        const int planes = (p.src1 != kNone) + (p.src2 != kNone);
+                        if (planes > 0) mbar_expect_tx(&src_full[buf], planes * kPlaneBytes);
+                        else mbar_arrive(&src_full[buf]);
+                        if (p.src1 != kNone) tma_load<1>(slab, &run.wide[p.src1], col, row, at.b, bar);
+                        if (p.src2 != kNone) tma_load<1>(slab + kPlaneBytes, &run.wide[p.src2], col, row, at.b, bar);
+                        if (used < kSlabs) ++used;
+                        if (++buf == kSlabs) {
+                            buf = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+            if (late) {
+                bool pending = false;
+                for (int q = 0; q < used; ++q) {
+                    const int s = (buf + kSlabs - 1 - q) % kSlabs;
+                    pending |= !mbar_wait(&src_full[s], s < buf ? phase : phase ^ 1u);
+                }
+                if (run.flags != nullptr)
+                    atomicOr(run.flags, kFlagTimeout | (pending ? kFlagCopyPending : 0u));
+            }
+        }
+        __syncwarp();
+    } else if (warp == 7) {
+        if (lane == 0) {   // stores
+            int buf = 0;
+            uint32_t phase = 0;
+            for (int ph = 0; ph < run.num_phases && !late; ++ph) {
+                const Phase p = run.phases[ph];
+                const int units = T::units(run.m, run.batch, p);
+                for (int u = group; u < units && !late; u += groups) {
+                    const UnitAt at = T::at(run.m, p, u);
+                    const int row0 = at.i * T::kTile + rank * kBlock;
+                    for (int s = at.slab0; s < at.slab1 && row0 < run.m; ++s) {
+                        const int col0 = at.j * T::kTile + s * kSlab;
+                        if (col0 >= p.n) break;
+                        if (!mbar_wait(&done[buf], phase)) {
+                            late = true;
+                            break;
+                        }
+                        const unsigned char* slab = slabs + buf * kSlabBytes;
+                        if (p.result != kPartial) {
+                            const bool transposed = p.result == kBf16Transposed;
+                            if (!transposed) tma_store(&run.wide[p.dst], slab, col0, row0, at.b);
+                            if (p.result == kState)
+                                tma_store(&run.wide[p.dst_lo], slab + kPlaneBytes, col0, row0, at.b);
+                            if (transposed || (p.sym && at.i != at.j)) {
+                                tma_store(&run.narrow[p.dst], slab + 2 * kPlaneBytes, row0, col0, at.b);
+                                if (row0 + 64 < run.m)
+                                    tma_store(&run.narrow[p.dst], slab + 2 * kPlaneBytes + kSlab * 128,
+                                              row0 + 64, col0, at.b);
+                            }
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        }
+                        mbar_arrive(&src_empty[buf]);
+                        if (++buf == kSlabs) {
+                            buf = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                // this CTA's results of the phase are in memory
+                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                if (!late) {
+                    fence_async_all();
+                    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(run.arrived + ph) : "memory");
+                }
+            }
+            if (late && run.flags != nullptr) atomicOr(run.flags, kFlagTimeout);
+        }
+        __syncwarp();
+    } else {   // results
+        const int row_in = warp * 32 + lane;
+        int acc = 0, buf = 0;
+        uint32_t acc_phase = 0, phase = 0;
+        for (int ph = 0; ph < run.num_phases && !late; ++ph) {
+            const Phase p = run.phases[ph];
+            if (p.reduce) {
+                const bool ok = grid_wait(run.arrived + ph - 1, gridDim.x);
+                late = __any_sync(kAll, !ok);
+            }
+            const int units = T::units(run.m, run.batch, p);
+            for (int u = group; u < units && !late; u += groups) {
+                const UnitAt at = T::at(run.m, p, u);
+                const int row0 = at.i * T::kTile + rank * kBlock;
+                if (!p.reduce) {
+                    const bool ok = mbar_wait(&acc_full[acc], acc_phase);
+                    if (__any_sync(kAll, !ok)) {
+                        late = true;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                }
+                for (int s = at.slab0; s < at.slab1 && row0 < run.m; ++s) {
+                    const int col0 = at.j * T::kTile + s * kSlab;
+                    if (col0 >= p.n) break;
+                    float v[kSlab];
+                    if (!p.reduce) {
+                        const uint32_t from = tmem + (static_cast<uint32_t>(warp * 32) << 16) +
+                                              acc * kAccCols + s * kSlab;
+                        tmem_load_32(from, reinterpret_cast<uint32_t*>(v));
+                        tmem_load_32(from + 32, reinterpret_cast<uint32_t*>(v) + 32);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                    }
+                    const bool ok = mbar_wait(&src_full[buf], phase);
+                    if (__any_sync(kAll, !ok)) {
+                        late = true;
+                        break;
+                    }
+                    unsigned char* slab = slabs + buf * kSlabBytes;
+                    // where this thread's row of a unit's partial accumulators starts
+                    auto partial = [&](int unit) {
+                        return reinterpret_cast<float4*>(run.partials) +
+                               ((static_cast<int64_t>(unit) * kPair + rank) * (T::kTile / 4) +
+                                s * (kSlab / 4)) * kBlock + row_in;
+                    };
+                    if (p.result == kPartial) {
+                        float4* to = partial(u);
+#pragma unroll
+                        for (int c = 0; c < kSlab / 4; ++c)
+                            to[c * kBlock] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                        __threadfence();
+                    } else {
+                        if (p.reduce) {
+#pragma unroll
+                            for (int c = 0; c < kSlab; ++c) v[c] = 0.0f;
+                            for (int q = 0; q < p.splits; ++q) {   // in the order of K
+                                const float4* from = partial(at.tile * p.splits + q);
+#pragma unroll
+                                for (int c = 0; c < kSlab / 4; ++c) {
+                                    const float4 x = __ldcg(from + c * kBlock);
+                                    v[4 * c] = __fadd_rn(v[4 * c], x.x);
+                                    v[4 * c + 1] = __fadd_rn(v[4 * c + 1], x.y);
+                                    v[4 * c + 2] = __fadd_rn(v[4 * c + 2], x.z);
+                                    v[4 * c + 3] = __fadd_rn(v[4 * c + 3], x.w);
+                                }
+                            }
+                        }
+                        const bool mirror = p.sym && at.i != at.j;
+                        if (p.result == kState)
+                            finish_row<2, kState, false>(slab, row_in, v, p.f_acc, p.f1, p.f2);
+                        else if (p.result == kBf16)
+                            finish_row<2, kBf16, false>(slab, row_in, v, p.f_acc, p.f1, p.f2);
+                        else if (p.result == kBf16Transposed)
+                            finish_row<2, kBf16Transposed, false>(slab, row_in, v, p.f_acc, p.f1, p.f2);
+                        else if (p.src1 == kNone)
+                            mirror ? finish_row<0, kPlane, true>(slab, row_in, v, p.f_acc, 0.0f, 0.0f)
+                                   : finish_row<0, kPlane, false>(slab, row_in, v, p.f_acc, 0.0f, 0.0f);
+                        else if (p.src2 == kNone)
+                            mirror ? finish_row<1, kPlane, true>(slab, row_in, v, p.f_acc, p.f1, 0.0f)
+                                   : finish_row<1, kPlane, false>(slab, row_in, v, p.f_acc, p.f1, 0.0f);
+                        else
+                            mirror ? finish_row<2, kPlane, true>(slab, row_in, v, p.f_acc, p.f1, p.f2)
+                                   : finish_row<2, kPlane, false>(slab, row_in, v, p.f_acc, p.f1, p.f2);
+                        fence_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&done[buf]);
+                    if (++buf == kSlabs) {
+                        buf = 0;
                         phase ^= 1u;
                     }
                 }
                 if (late) break;
-                mma_commit(&acc_full[acc]);
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
-            }
-            if (late) {
-                mma_commit(drain);
-                mbar_wait(drain, 0);
-                if (g.flags != nullptr) atomicOr(g.flags, kFlagTimeout);
-            }
-        }
-        __syncwarp();
-    } else {
-        float* buf = epi + warp * 32 * kEpiPitch;
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        for (int t = blockIdx.x; t < g.total_tiles; t += gridDim.x) {
-            if (!mbar_wait(&acc_full[acc], acc_phase)) s_late = 1;
-            __syncwarp();
-            if (*static_cast<volatile uint32_t*>(&s_late) != 0) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const TileAt at = tile_at<kSym, kTileN>(g, t);
-            const int row0 = at.i * kTileM + warp * 32;
-            for (int c = 0; c < kTileN; c += kEpiCols) {
-                const int col0 = at.j * kTileN + c;
-                if (col0 >= g.n || row0 >= g.m || (kSym && col0 > row0 + 31)) break;
-#pragma unroll
-                for (int h = 0; h < kEpiCols / 32; ++h) {
-                    uint32_t v[32];
-                    tmem_load_32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + acc * kTileN + c + h * 32, v);
-                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) buf[lane * kEpiPitch + h * 32 + i] = __uint_as_float(v[i]);
+                if (!p.reduce) {
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (kPair == 2) arrive_at(leader_addr(&acc_empty[acc]));
+                        else mbar_arrive(&acc_empty[acc]);
+                    }
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
                 }
-                __syncwarp();
-                epilogue_step<kMode>(g, buf, at.b, row0, col0, lane);
-                __syncwarp();
             }
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            if (lane == 0) mbar_arrive(&acc_empty[acc]);
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
         }
+        if (late && lane == 0 && run.flags != nullptr) atomicOr(run.flags, kFlagTimeout);
     }
     __syncthreads();
-    if (warp == 5)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmemCols));
+    if constexpr (kPair == 2) {   // no copy, arrival or product of the pair is left
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    if (warp == 5) {
+        if constexpr (kPair == 2)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(2 * kAccCols));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(2 * kAccCols));
+    }
+}
+
+// The state's planes to bf16, transposed back where the matrix is tall: for outputs whose rows
+// are no whole 16 bytes, which a TMA store cannot address.
+__global__ void __launch_bounds__(256)
+k_orth_finish(const __half* __restrict__ hi, const __half* __restrict__ lo, int64_t ld, int64_t plane,
+              int64_t m, int64_t n, float f, uint16_t* __restrict__ out, bool tall) {
+    __shared__ float s_tile[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t b = blockIdx.z, r0 = static_cast<int64_t>(blockIdx.y) * 32,
+                  c0 = static_cast<int64_t>(blockIdx.x) * 32;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = r0 + warp + 8 * i, c = c0 + lane;
+        if (r >= m || c >= n || !SPL_CHECK(c < ld, kSiteOrthState, c)) continue;
+        const int64_t at = b * plane + r * ld + c;
+        const float x = __fmul_rn(f, __fmaf_rn(__half2float(lo[at]), 1.0f / kLoScale, __half2float(hi[at])));
+        if (tall) s_tile[warp + 8 * i][lane] = x;
+        else Vec16<true>::store1(out, (b * m + r) * n + c, x);
+    }
+    if (!tall) return;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = r0 + lane, c = c0 + warp + 8 * i;
+        if (r < m && c < n && SPL_CHECK(c < n, kSiteOrthOut, c))
+            Vec16<true>::store1(out, (b * n + c) * m + r, s_tile[lane][warp + 8 * i]);
+    }
 }
 
 // ---- host -----------------------------------------------------------------------------------
@@ -594,26 +995,11 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// Tensor map over fp16 [batch][rows][cols] with row pitch ld, boxes of 64 columns x box_rows.
-bool make_map(CUtensorMap* map, __half* base, int64_t batch, int64_t rows, int64_t cols, int64_t ld,
-              int box_rows) {
-    const EncodeTiled enc = encode_tiled();
-    if (enc == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
-                                static_cast<cuuint64_t>(batch)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(rows * ld * 2)};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-    const cuuint32_t step[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, step,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct OrthLayout {
-    int64_t m, n, ldx, ldm;   // short and long side, row pitches of X and of A and B
-    size_t hi[2], lo[2], a, b, partials, bytes;
+    int64_t m, n, ldx, ldm;   // short and long side, row pitches of X and of the square matrices
+    size_t hi[2], lo[2], square[2], arrived, partials, norms, bytes;
 };
 
 OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
@@ -633,32 +1019,86 @@ OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
         l.hi[i] = take(plane);
         l.lo[i] = take(plane);
     }
-    l.a = take(static_cast<size_t>(batch * l.m * l.ldm) * 2);
-    l.b = take(static_cast<size_t>(batch * l.m * l.ldm) * 2);
-    l.partials = take(static_cast<size_t>(batch) * kMaxPartials * sizeof(double));
+    for (int i = 0; i < 2; ++i) l.square[i] = take(static_cast<size_t>(batch * l.m * l.ldm) * 2);
+    l.arrived = take(kMaxPhases * 4);
+    l.partials = 0;
+    l.norms = take(static_cast<size_t>(batch) * kMaxPartials * sizeof(double));
     l.bytes = at;
     return l;
 }
 
-template <int kMode, int kTileN>
-cudaError_t launch_product(const CUtensorMap& a, const CUtensorMap& b, GemmArgs g, int sms,
-                           cudaStream_t stream) {
-    using S = GemmShape<kTileN>;
-    constexpr bool kSym = kMode == kGram || kMode == kPoly;
-    g.tiles_m = (g.m + kTileM - 1) / kTileM;
-    g.tiles_n = (g.n + kTileN - 1) / kTileN;
-    g.tiles = g.tiles_m * g.tiles_n;
-    if (kSym) {
-        g.tiles = 0;
-        for (int i = 0; i < g.tiles_m; ++i) g.tiles += i / (kTileN / kTileM) + 1;
-    }
-    g.total_tiles = g.tiles * g.batch;
-    const void* kern = reinterpret_cast<const void*>(&k_orth_product<kMode, kTileN>);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+// What a launch of the run kernel depends on beside its arguments, found once per device.
+struct RunLimits {
+    int single, pairs;   // CTAs, and pairs of CTAs, resident at once
+};
+
+template <int kPair>
+cudaError_t prepare_run(int sms, int* groups) {
+    const void* kern = reinterpret_cast<const void*>(&k_orth_run<kPair>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRunSmem);
     if (e != cudaSuccess) return e;
-    const int grid = g.total_tiles < sms ? g.total_tiles : sms;
-    k_orth_product<kMode, kTileN><<<grid, kGemmThreads, S::kSmem, stream>>>(a, b, g);
-    return cudaGetLastError();
+    if (kPair == 1) {
+        *groups = sms;
+        return cudaSuccess;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
+    cfg.blockDim = dim3(kRunThreads);
+    cfg.dynamicSmemBytes = kRunSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(groups, kern, &cfg);
+}
+
+cudaError_t run_limits(RunLimits* out) {
+    static std::mutex mu;
+    static RunLimits cached[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (cached[dev].single == 0) {
+        int sms = 0;
+        RunLimits l = {};
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = prepare_run<1>(sms, &l.single);
+        if (e == cudaSuccess) e = prepare_run<2>(sms, &l.pairs);
+        if (e != cudaSuccess) return e;
+        cached[dev] = l;
+    }
+    *out = cached[dev];
+    return cudaSuccess;
+}
+
+template <int kPair>
+cudaError_t launch_run(const OrthRun& run, int groups, cudaStream_t stream) {
+    using T = Tiling<kPair>;
+    int most = 1;
+    for (int i = 0; i < run.num_phases; ++i) {
+        const int u = T::units(run.m, run.batch, run.phases[i]);
+        if (u > most) most = u;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((most < groups ? most : groups) * kPair));
+    cfg.blockDim = dim3(kRunThreads);
+    cfg.dynamicSmemBytes = kRunSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kPair;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_orth_run<kPair>, run);
 }
 
 }  // namespace
@@ -675,14 +1115,11 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& a, bool bf16, cudaStre
     const OrthLayout l = orth_layout(a.batch, a.rows, a.cols);
     unsigned char* ws = static_cast<unsigned char*>(a.workspace);
     const bool tall = a.rows > a.cols;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    RunLimits limits;
+    cudaError_t e = run_limits(&limits);
     if (e != cudaSuccess) return e;
-    __half* hi[2] = {reinterpret_cast<__half*>(ws + l.hi[0]), reinterpret_cast<__half*>(ws + l.hi[1])};
-    __half* lo[2] = {reinterpret_cast<__half*>(ws + l.lo[0]), reinterpret_cast<__half*>(ws + l.lo[1])};
-    __half* gram = reinterpret_cast<__half*>(ws + l.a);
-    __half* poly = reinterpret_cast<__half*>(ws + l.b);
+    const EncodeTiled encode = encode_tiled();
+    if (encode == nullptr) return cudaErrorNotSupported;
 
     PrepArgs p = {};
     p.update = a.update;
@@ -695,83 +1132,107 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& a, bool bf16, cudaStre
     p.nesterov = a.nesterov;
     p.eps = a.eps;
     p.x_scale = std::ldexp(1.0f, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(l.n)))));
-    p.partials = reinterpret_cast<double*>(ws + l.partials);
-    p.num_partials = static_cast<int>(a.rows < kMaxPartials ? a.rows : kMaxPartials);
-    p.hi = hi[0];
-    p.lo = lo[0];
+    p.partials = reinterpret_cast<double*>(ws + l.norms);
+    p.hi = reinterpret_cast<__half*>(ws + l.hi[0]);
+    p.lo = reinterpret_cast<__half*>(ws + l.lo[0]);
     p.ld = l.ldx;
     p.plane = l.m * l.ldx;
+    p.arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
     p.flags = a.flags;
-    const dim3 norm_grid(static_cast<unsigned>(p.num_partials), static_cast<unsigned>(a.batch));
-    const dim3 state_grid(static_cast<unsigned>((a.cols + 31) / 32), static_cast<unsigned>((a.rows + 31) / 32),
-                          static_cast<unsigned>(a.batch));
-    if (bf16) {
-        k_orth_norm<true><<<norm_grid, kPrepThreads, 0, stream>>>(p);
-        if (tall) k_orth_state<true, true><<<state_grid, kPrepThreads, 0, stream>>>(p);
-        else k_orth_state<true, false><<<state_grid, kPrepThreads, 0, stream>>>(p);
-    } else {
-        k_orth_norm<false><<<norm_grid, kPrepThreads, 0, stream>>>(p);
-        if (tall) k_orth_state<false, true><<<state_grid, kPrepThreads, 0, stream>>>(p);
-        else k_orth_state<false, false><<<state_grid, kPrepThreads, 0, stream>>>(p);
-    }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int size = bf16 ? 2 : 4, lanes = 16 / size;
+    const bool vec = reinterpret_cast<uintptr_t>(a.update) % 16 == 0 && a.cols % lanes == 0 &&
+                     a.row_stride % lanes == 0 && (a.batch == 1 || a.batch_stride % lanes == 0) &&
+                     reinterpret_cast<uintptr_t>(a.momentum) % 16 == 0;
+    if (bf16) e = vec ? launch_prep<true, true>(p, a.batch, tall, limits.single, stream)
+                      : launch_prep<true, false>(p, a.batch, tall, limits.single, stream);
+    else e = vec ? launch_prep<false, true>(p, a.batch, tall, limits.single, stream)
+                 : launch_prep<false, false>(p, a.batch, tall, limits.single, stream);
+    if (e != cudaSuccess) return e;
 
-    CUtensorMap x_k[2], x_n[2], gram_k, poly_k;   // operands with rows along K, and X along N
-    for (int i = 0; i < 2; ++i)
-        if (!make_map(&x_k[i], hi[i], a.batch, l.m, l.n, l.ldx, 128) ||
-            !make_map(&x_n[i], hi[i], a.batch, l.m, l.n, l.ldx, 64))
-            return cudaErrorInvalidValue;
-    if (!make_map(&gram_k, gram, a.batch, l.m, l.m, l.ldm, 128) ||
-        !make_map(&poly_k, poly, a.batch, l.m, l.m, l.ldm, 128))
-        return cudaErrorInvalidValue;
-
-    constexpr int kN = 256;
-    for (int s = 0; s < a.steps; ++s) {
-        const int x = s & 1;
-        GemmArgs g = {};
-        g.batch = static_cast<int>(a.batch);
-        g.flags = a.flags;
-        g.m = static_cast<int>(l.m);
-        g.n = g.m;
-        g.k = static_cast<int>(l.n);
-        g.fb = kGramScale / (p.x_scale * p.x_scale);
-        g.dst_hi = gram;
-        g.dst_ld = l.ldm;
-        g.dst_plane = l.m * l.ldm;
-        if ((e = launch_product<kGram, kN>(x_k[x], x_k[x], g, sms, stream)) != cudaSuccess) return e;
-        g.k = g.m;
-        g.fa = a.coef[1];
-        g.fb = a.coef[2] / kGramScale;
-        g.src_hi = gram;
-        g.src_ld = l.ldm;
-        g.src_plane = l.m * l.ldm;
-        g.dst_hi = poly;
-        if ((e = launch_product<kPoly, kN>(gram_k, gram_k, g, sms, stream)) != cudaSuccess) return e;
-        g.n = static_cast<int>(l.n);
-        g.fa = a.coef[0];
-        g.fb = 1.0f / kGramScale;
-        g.src_hi = hi[x];
-        g.src_lo = lo[x];
-        g.src_ld = l.ldx;
-        g.src_plane = l.m * l.ldx;
-        g.dst_hi = hi[x ^ 1];
-        g.dst_lo = lo[x ^ 1];
-        g.dst_ld = l.ldx;
-        g.dst_plane = l.m * l.ldx;
-        if (s + 1 < a.steps) {
-            e = launch_product<kUpdate, kN>(poly_k, x_n[x], g, sms, stream);
-        } else {
-            g.fa /= p.x_scale;
-            g.fb /= p.x_scale;
-            g.out = a.out;
-            g.out_ld = a.cols;
-            g.out_plane = a.rows * a.cols;
-            g.tall = tall;
-            e = launch_product<kLast, kN>(poly_k, x_n[x], g, sms, stream);
+    static thread_local OrthRun run;   // large for a stack frame; filled anew each call
+    bool mapped = true;
+    // Tensor maps of matrix `id`: 16-bit values [batch][rows][cols], row pitch ld.
+    auto matrix = [&](int id, void* base, CUtensorMapDataType type, int64_t rows, int64_t cols, int64_t ld) {
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                                    static_cast<cuuint64_t>(a.batch)};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(rows * ld * 2)};
+        const cuuint32_t step[3] = {1, 1, 1};
+        for (int i = 0; i < 2; ++i) {
+            const cuuint32_t box[3] = {64, i == 0 ? 128u : 64u, 1};
+            mapped &= encode(i == 0 ? &run.wide[id] : &run.narrow[id], type, 3, base, dims, strides, box, step,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
         }
-        if (e != cudaSuccess) return e;
+    };
+    enum : uint8_t { kHi0, kHi1, kLo0, kLo1, kA, kB, kOut };
+    const auto f16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    for (int i = 0; i < 2; ++i) {
+        matrix(kHi0 + i, ws + l.hi[i], f16, l.m, l.n, l.ldx);
+        matrix(kLo0 + i, ws + l.lo[i], f16, l.m, l.n, l.ldx);
+        matrix(kA + i, ws + l.square[i], f16, l.m, l.m, l.ldm);
     }
-    return cudaSuccess;
+    const bool direct = a.cols % 8 == 0;   // the output's rows are whole 16 bytes
+    if (direct) matrix(kOut, a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.rows, a.cols, a.cols);
+    if (!mapped) return cudaErrorInvalidValue;
+
+    run.m = static_cast<int>(l.m);
+    run.batch = static_cast<int>(a.batch);
+    run.partials = nullptr;
+    run.arrived = p.arrived;
+    run.flags = a.flags;
+    run.num_phases = 0;
+    const int m = run.m, n = static_cast<int>(l.n);
+    auto add = [&](const Phase& ph) { run.phases[run.num_phases++] = ph; };
+    int x = 0;
+    for (int s = 0; s < a.steps; ++s, x ^= 1) {
+        const uint8_t hi = static_cast<uint8_t>(kHi0 + x), lo = static_cast<uint8_t>(kLo0 + x);
+        const bool last = s + 1 == a.steps && direct;
+        Phase ph = {};
+        ph.splits = 1;
+        // A = X X^T
+        ph.a = ph.b = hi;
+        ph.src1 = ph.src2 = ph.dst_lo = kNone;
+        ph.dst = kA;
+        ph.result = kPlane;
+        ph.sym = true;
+        ph.n = m;
+        ph.k = n;
+        ph.f_acc = kGramScale / (p.x_scale * p.x_scale);
+        add(ph);
+        // B = b A + c A A
+        ph.a = ph.b = ph.src1 = kA;
+        ph.dst = kB;
+        ph.k = m;
+        ph.f_acc = a.coef[2] / kGramScale;
+        ph.f1 = a.coef[1];
+        add(ph);
+        // X = a X + B X
+        ph.a = kB;
+        ph.b = ph.src1 = hi;
+        ph.src2 = lo;
+        ph.dst = last ? static_cast<uint8_t>(kOut) : static_cast<uint8_t>(kHi0 + (x ^ 1));
+        ph.dst_lo = last ? kNone : static_cast<uint8_t>(kLo0 + (x ^ 1));
+        ph.result = !last ? kState : tall ? kBf16Transposed : kBf16;
+        ph.sym = false;
+        ph.b_along_n = true;
+        ph.n = n;
+        const float f = last ? 1.0f / p.x_scale : 1.0f;
+        ph.f_acc = f / kGramScale;
+        ph.f1 = f * a.coef[0];
+        ph.f2 = ph.f1 / kLoScale;
+        add(ph);
+    }
+    // Pairs of CTAs once their 256 x 256 tiles give every pair of SMs some
+    const bool pairs = Tiling<2>::units(m, run.batch, run.phases[2]) >= limits.pairs;
+    e = pairs ? launch_run<2>(run, limits.pairs, stream) : launch_run<1>(run, limits.single, stream);
+    if (e != cudaSuccess || direct) return e;
+    const dim3 grid(static_cast<unsigned>((l.n + 31) / 32), static_cast<unsigned>((l.m + 31) / 32),
+                    static_cast<unsigned>(a.batch));
+    k_orth_finish<<<grid, 256, 0, stream>>>(reinterpret_cast<const __half*>(ws + l.hi[x]),
+                                            reinterpret_cast<const __half*>(ws + l.lo[x]), l.ldx,
+                                            l.m * l.ldx, l.m, l.n, 1.0f / p.x_scale, a.out, tall);
+    return cudaGetLastError();
 }
 
 }  // namespace spl

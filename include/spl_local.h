@@ -130,8 +130,10 @@ size_t spl_orthogonalize_workspace(size_t batch, size_t rows, size_t cols);
  * update:   [batch][rows][cols] of `dtype`; row_stride >= cols, batch_stride between matrices
  * momentum: [batch][rows][cols] fp32, contiguous, or NULL (mu and nesterov are then ignored)
  * steps:    1 .. 32;  coefficients: 3 finite values of at most 8 in size
- * out:      [batch][rows][cols] bf16, contiguous
- * batch, rows, cols: >= 1; batch <= 65535, rows and cols <= 2^20
+ * out:      [batch][rows][cols] bf16, contiguous, 16-byte aligned; out and workspace are device
+ *           memory
+ * batch, rows, cols: >= 1; batch <= 65535, rows and cols <= 2^20, and
+ *           batch * rows * cols * min(rows, cols) <= 2^46
  * SPL_FLAG_TIMEOUT as for the codec calls, if a bulk copy does not land in bounded time.
  */
 spl_status spl_orthogonalize(const void* update, spl_dtype dtype, size_t batch, size_t rows,

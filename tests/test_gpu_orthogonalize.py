@@ -52,6 +52,16 @@ def test_matrix(m, n, dtype):
     assert off(got, iterate(u)) <= limit(m, n)
 
 
+@pytest.mark.parametrize("batch,m,n", [(12, 520, 1100), (3, 2100, 2300), (1, 2560, 3000)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_many_tiles(batch, m, n, tall):
+    """Enough 256 x 256 tiles for pairs of CTAs, ragged ones among them."""
+    u = torch.randn(batch, *((n, m) if tall else (m, n)), generator=gen(m), device=DEV)
+    got, ref = spl.orthogonalize(u), iterate(u)
+    for i in range(batch):
+        assert off(got[i], ref[i]) <= limit(m, n)
+
+
 @pytest.mark.parametrize("power", [0.0, 0.5, 1.0, 1.5, 2.0])
 @pytest.mark.parametrize("m,n", [(256, 256), (300, 900)])
 def test_spread_of_singular_values(m, n, power):
