@@ -286,8 +286,8 @@ cudaError_t launch_prep(PrepArgs p, int64_t batch, bool tall, int sms, cudaStrea
 }
 
 // ---- the products ---------------------------------------------------------------------------
-// All products of a call run in one persistent cooperative kernel, as a list of phases with a
-// barrier over the grid between them.  A phase computes D = A B^T (B's rows along K) or D = A B
+// All products of a call run in one persistent cooperative kernel, as a list of phases.  A phase
+// names the earlier one that every CTA must have finished (a counter per phase in the workspace).  A phase computes D = A B^T (B's rows along K) or D = A B
 // (B's rows along N) tile by tile, and for each tile
 //
 //   value = f_acc * accumulator + f1 * source1 + f2 * source2
@@ -316,7 +316,7 @@ constexpr int kSlabBytes = 3 * kPlaneBytes;  // two source planes, replaced by r
 constexpr int kSlabs = 2;
 constexpr int kRunThreads = 256;
 constexpr int kRunSmem = kStages * kStageBytes + kSlabs * kSlabBytes + 1024;
-constexpr int kMaxMatrices = 12;
+constexpr int kMaxMatrices = 10;   // X's planes twice, the output, five m x m matrices
 constexpr uint8_t kNone = 255;
 
 enum ResultKind : uint8_t { kPlane, kState, kBf16, kBf16Transposed, kPartial };
@@ -327,6 +327,8 @@ struct Phase {
     bool b_along_n, sym;
     bool reduce;      // sum the previous phase's partial accumulators instead of a product
     uint8_t splits;   // parts of K (results are kPartial unless 1); of a reduce: partials per tile
+    int16_t after;    // the phase that must be complete before this one, or -1
+    int16_t first;    // the group of CTAs that takes the first unit
     int n, k;         // columns of the result, length of the product
     float f_acc, f1, f2;
 };
@@ -632,13 +634,13 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
             for (int ph = 0; ph < run.num_phases && !late; ++ph) {
                 const Phase p = run.phases[ph];
                 if (p.reduce) continue;
-                if (ph > 0 && !grid_wait(run.arrived + ph - 1, gridDim.x)) {
+                if (p.after >= 0 && !grid_wait(run.arrived + p.after, gridDim.x)) {
                     late = true;
                     break;
                 }
                 fence_async_all();
                 const int units = T::units(run.m, run.batch, p);
-                for (int u = group; u < units && !late; u += groups) {
+                for (int u = (group + groups - p.first) % groups; u < units && !late; u += groups) {
                     const UnitAt at = T::at(run.m, p, u);
                     for (int kb = at.k0; kb < at.k1; ++kb) {
                         if (!mbar_wait(&empty[stage], phase ^ 1u)) {
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                 const uint32_t lead = p.b_along_n ? kOperandBytes / 2 : 16;
                 const uint32_t b_step = p.b_along_n ? 128 : 2;   // 16 of K: 16 rows, or 32 bytes
                 const int units = T::units(run.m, run.batch, p);
-                for (int u = group; u < units && !late; u += groups) {
+                for (int u = (group + groups - p.first) % groups; u < units && !late; u += groups) {
                     const UnitAt at = T::at(run.m, p, u);
                     if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u)) {
                         late = true;
@@ -736,13 +738,13 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
             uint32_t phase = 0;
             for (int ph = 0; ph < run.num_phases && !late; ++ph) {
                 const Phase p = run.phases[ph];
-                if (ph > 0 && !grid_wait(run.arrived + ph - 1, gridDim.x)) {
+                if (p.after >= 0 && !grid_wait(run.arrived + p.after, gridDim.x)) {
                     late = true;
                     break;
                 }
                 fence_async_all();
                 const int units = T::units(run.m, run.batch, p);
-                for (int u = group; u < units && !late; u += groups) {
+                for (int u = (group + groups - p.first) % groups; u < units && !late; u += groups) {
                     const UnitAt at = T::at(run.m, p, u);
                     const int row = at.i * T::kTile + rank * kBlock;
                     if (row >= run.m) continue;
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
             for (int ph = 0; ph < run.num_phases && !late; ++ph) {
                 const Phase p = run.phases[ph];
                 const int units = T::units(run.m, run.batch, p);
-                for (int u = group; u < units && !late; u += groups) {
+                for (int u = (group + groups - p.first) % groups; u < units && !late; u += groups) {
                     const UnitAt at = T::at(run.m, p, u);
                     const int row0 = at.i * T::kTile + rank * kBlock;
                     for (int s = at.slab0; s < at.slab1 && row0 < run.m; ++s) {
@@ -835,11 +837,11 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
         for (int ph = 0; ph < run.num_phases && !late; ++ph) {
             const Phase p = run.phases[ph];
             if (p.reduce) {
-                const bool ok = grid_wait(run.arrived + ph - 1, gridDim.x);
+                const bool ok = grid_wait(run.arrived + p.after, gridDim.x);
                 late = __any_sync(kAll, !ok);
             }
             const int units = T::units(run.m, run.batch, p);
-            for (int u = group; u < units && !late; u += groups) {
+            for (int u = (group + groups - p.first) % groups; u < units && !late; u += groups) {
                 const UnitAt at = T::at(run.m, p, u);
                 const int row0 = at.i * T::kTile + rank * kBlock;
                 if (!p.reduce) {
@@ -997,9 +999,18 @@ EncodeTiled encode_tiled() {
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
+constexpr int kSquares = 5;      // m x m matrices: A, and the polynomials of a group of steps
+constexpr int kSplitUnits = 320; // partial 128 x 128 accumulators a split product may leave
+constexpr int kMaxSplits = 16;   // parts of a long K
+constexpr int kSplitBlocks = 4;  // of at least 4 blocks each
+
+// Whether a group of steps pays for a matrix of these sides (see group_steps).
+bool may_group(int64_t m, int64_t n) { return 4 * n >= 5 * m && m >= 256; }
+
 struct OrthLayout {
     int64_t m, n, ldx, ldm;   // short and long side, row pitches of X and of the square matrices
-    size_t hi[2], lo[2], square[2], arrived, partials, norms, bytes;
+    size_t hi[2], lo[2], square[kSquares], arrived, partials, norms, bytes;
+    size_t partial_bytes;
 };
 
 OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
@@ -1019,9 +1030,20 @@ OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
         l.hi[i] = take(plane);
         l.lo[i] = take(plane);
     }
-    for (int i = 0; i < 2; ++i) l.square[i] = take(static_cast<size_t>(batch * l.m * l.ldm) * 2);
+    const int squares = may_group(l.m, l.n) ? kSquares : 2;
+    for (int i = 0; i < kSquares; ++i)
+        l.square[i] = i < squares ? take(static_cast<size_t>(batch * l.m * l.ldm) * 2) : 0;
     l.arrived = take(kMaxPhases * 4);
-    l.partials = 0;
+    // partial accumulators of a split product: enough units for a few per SM, where its tiles
+    // alone are fewer than that
+    const int64_t blocks = (l.n + kTileK - 1) / kTileK, tm = (l.m + kBlock - 1) / kBlock;
+    const int64_t tiles = tm * (tm + 1) / 2 * batch;
+    const int64_t splits = blocks / kSplitBlocks < kMaxSplits ? blocks / kSplitBlocks : kMaxSplits;
+    l.partial_bytes = 0;
+    if (tiles < kSplitUnits && splits > 1)
+        l.partial_bytes = static_cast<size_t>(tiles * splits < kSplitUnits ? tiles * splits : kSplitUnits) *
+                          kBlock * kBlock * 4;
+    l.partials = take(l.partial_bytes);
     l.norms = take(static_cast<size_t>(batch) * kMaxPartials * sizeof(double));
     l.bytes = at;
     return l;
@@ -1074,6 +1096,116 @@ cudaError_t run_limits(RunLimits* out) {
     }
     *out = cached[dev];
     return cudaSuccess;
+}
+
+// How many of the first steps are taken as one polynomial of A, applied to X once.  Per step X
+// costs 3 m^2 n multiplications (the symmetric product counts half) and A m^3; a group of g costs
+// 3 m^2 n + (4 g - 3) m^3, less as soon as n > m.  The iteration's last steps undo the roundings
+// of its first ones, so only those are grouped, and at least two steps stay single: 64-bit
+// simulations with these roundings give errors of 1.0e-3 to 1.8e-3 for steps one by one, the same
+// for a group of 2, and for a group of 3 the same once m >= 1024 (at most 1.4e-3) but up to 2.1e-3
+// at m = 512 and 5e-3 at 64; two groups of 2 would give up to 2.8e-3 at m = 512.
+// The 28672 x 8192 matrix: 22.0 ms one by one.
+int group_steps(int64_t m, int64_t n, int steps, float a) {
+    if (!may_group(m, n)) return 1;
+    int size = m >= 1024 ? 3 : 2;
+    if (steps - 2 < size) size = steps - 2;
+    // R is as large as the identity's factor a^size, and must fit fp16 times its scale
+    while (size > 1 && std::pow(std::fabs(a), size) > 48.0f) --size;
+    return size > 1 ? size : 1;
+}
+
+struct PhaseList {
+    Phase phases[kMaxPhases];
+    int num;
+
+    int16_t last() const { return static_cast<int16_t>(num - 1); }
+    void add(Phase ph) {
+        ph.splits = 1;
+        ph.after = last();
+        phases[num++] = ph;
+    }
+    void after(int16_t phase) { phases[num - 1].after = phase; }
+    // A symmetric m x m product.
+    void square(uint8_t a, uint8_t b, uint8_t src1, uint8_t src2, uint8_t dst, int m, int k, float f_acc,
+                float f1, float f2) {
+        Phase ph = {};
+        ph.a = a;
+        ph.b = b;
+        ph.src1 = src1;
+        ph.src2 = src2;
+        ph.dst = dst;
+        ph.dst_lo = kNone;
+        ph.result = kPlane;
+        ph.sym = true;
+        ph.n = m;
+        ph.k = k;
+        ph.f_acc = f_acc;
+        ph.f1 = f1;
+        ph.f2 = f2;
+        add(ph);
+    }
+};
+
+// Estimated microseconds of a list of products on `groups` CTAs (or pairs), and with `out` the
+// phases to run: a symmetric product with fewer tiles than groups and a long K is split along K
+// where that pays, followed by a phase that sums the parts.  Measured: a block of 64 along K 0.14
+// us for a 128 x 128 tile and 0.27 us for a pair's 256 x 256 one, an epilogue of 128 columns 1.2 us,
+// and 4 us from a phase's last result to the next one's first product.
+template <int kPair>
+double plan(const PhaseList& list, const OrthRun& run, int groups, size_t partial_bytes, OrthRun* out) {
+    using T = Tiling<kPair>;
+    const double block = kPair == 2 ? 0.27 : 0.14, epilogue = 1.2 * kPair, between = 4.0;
+    const size_t unit_bytes = static_cast<size_t>(T::kTile) * T::kTile * 4;
+    double total = 0.0;
+    int index[kMaxPhases], num = 0, taken = 0;   // where each listed phase ends up
+    bool split = false;
+    for (int i = 0; i < list.num; ++i) {
+        Phase ph = list.phases[i];
+        const int tiles = T::tiles(run.m, ph) * run.batch, blocks = (ph.k + kTileK - 1) / kTileK;
+        auto time = [&](int splits) {
+            const int units = tiles * splits, waves = (units + groups - 1) / groups;
+            const double one = block * ((blocks + splits - 1) / splits);
+            double t = waves * (one > epilogue ? one : epilogue) + epilogue + between;
+            if (splits > 1) {
+                const int slabs = tiles * T::kTileSlabs;
+                t += (slabs + groups - 1) / groups * (1.0 + 0.25 * splits) + between;
+            }
+            return t;
+        };
+        int best = 1;
+        if (ph.sym)
+            for (int q = 2; q <= kMaxSplits && q <= blocks / kSplitBlocks; ++q)
+                if (static_cast<size_t>(tiles) * q * unit_bytes <= partial_bytes && num + 3 < kMaxPhases &&
+                    time(q) < time(best))
+                    best = q;
+        total += time(best);
+        // the parts of two products beside each other would share the partials' memory
+        if (i > 0 && (best > 1 || split)) ph.after = static_cast<int16_t>(i - 1);
+        split = best > 1;
+        const bool beside = ph.after >= 0 && ph.after != i - 1;
+        ph.after = static_cast<int16_t>(ph.after < 0 ? -1 : index[ph.after]);
+        ph.first = static_cast<int16_t>(beside ? taken % groups : 0);
+        Phase sum = ph;
+        if (best > 1) {
+            ph.splits = static_cast<uint8_t>(best);
+            ph.result = kPartial;
+            ph.src1 = ph.src2 = kNone;
+        }
+        taken = ph.first + tiles * best;
+        if (out != nullptr) out->phases[num] = ph;
+        index[i] = num++;
+        if (best > 1) {
+            sum.reduce = true;
+            sum.splits = static_cast<uint8_t>(best);
+            sum.after = static_cast<int16_t>(num - 1);
+            sum.first = 0;
+            if (out != nullptr) out->phases[num] = sum;
+            index[i] = num++;
+        }
+    }
+    if (out != nullptr) out->num_phases = num;
+    return total;
 }
 
 template <int kPair>
@@ -1165,67 +1297,99 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& a, bool bf16, cudaStre
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
         }
     };
-    enum : uint8_t { kHi0, kHi1, kLo0, kLo1, kA, kB, kOut };
+    enum : uint8_t { kHi0, kHi1, kLo0, kLo1, kOut, kSquare0 };
     const auto f16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     for (int i = 0; i < 2; ++i) {
         matrix(kHi0 + i, ws + l.hi[i], f16, l.m, l.n, l.ldx);
         matrix(kLo0 + i, ws + l.lo[i], f16, l.m, l.n, l.ldx);
-        matrix(kA + i, ws + l.square[i], f16, l.m, l.m, l.ldm);
     }
+    const int grouped = group_steps(l.m, l.n, a.steps, a.coef[0]);
+    for (int i = 0; i < (grouped > 1 ? kSquares : 2); ++i)
+        matrix(kSquare0 + i, ws + l.square[i], f16, l.m, l.m, l.ldm);
     const bool direct = a.cols % 8 == 0;   // the output's rows are whole 16 bytes
     if (direct) matrix(kOut, a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.rows, a.cols, a.cols);
     if (!mapped) return cudaErrorInvalidValue;
 
     run.m = static_cast<int>(l.m);
     run.batch = static_cast<int>(a.batch);
-    run.partials = nullptr;
+    run.partials = reinterpret_cast<float*>(ws + l.partials);
     run.arrived = p.arrived;
     run.flags = a.flags;
-    run.num_phases = 0;
+
+    // The list of products.  With f the identity's factor, X <- f X + R X where R is the rest of
+    // the polynomial of one step (R = B, f = a) or of a group of them.
+    PhaseList list = {};
+    uint8_t free_squares[kSquares];
+    int num_free = 0;
+    for (int i = (grouped > 1 ? kSquares : 2) - 1; i > 0; --i) free_squares[num_free++] = static_cast<uint8_t>(kSquare0 + i);
+    auto take = [&] { return free_squares[--num_free]; };
+    auto give = [&](uint8_t id) { free_squares[num_free++] = id; };
+    const uint8_t A = kSquare0;
     const int m = run.m, n = static_cast<int>(l.n);
-    auto add = [&](const Phase& ph) { run.phases[run.num_phases++] = ph; };
+    const float ca = a.coef[0];
     int x = 0;
-    for (int s = 0; s < a.steps; ++s, x ^= 1) {
+    for (int s = 0; s < a.steps; x ^= 1) {
+        const int size = s == 0 ? grouped : 1;
         const uint8_t hi = static_cast<uint8_t>(kHi0 + x), lo = static_cast<uint8_t>(kLo0 + x);
-        const bool last = s + 1 == a.steps && direct;
-        Phase ph = {};
-        ph.splits = 1;
         // A = X X^T
-        ph.a = ph.b = hi;
-        ph.src1 = ph.src2 = ph.dst_lo = kNone;
-        ph.dst = kA;
-        ph.result = kPlane;
-        ph.sym = true;
-        ph.n = m;
-        ph.k = n;
-        ph.f_acc = kGramScale / (p.x_scale * p.x_scale);
-        add(ph);
-        // B = b A + c A A
-        ph.a = ph.b = ph.src1 = kA;
-        ph.dst = kB;
-        ph.k = m;
-        ph.f_acc = a.coef[2] / kGramScale;
-        ph.f1 = a.coef[1];
-        add(ph);
-        // X = a X + B X
-        ph.a = kB;
+        list.square(hi, hi, kNone, kNone, A, m, n, kGramScale / (p.x_scale * p.x_scale), 0.0f, 0.0f);
+        uint8_t R = kNone;
+        float f = ca;
+        for (int i = 0; i < size; ++i) {
+            const bool more = i + 1 < size;
+            const uint8_t B = take();   // B = b A + c A A
+            list.square(A, A, A, kNone, B, m, m, a.coef[2] / kGramScale, a.coef[1], 0.0f);
+            const int16_t poly = list.last();
+            uint8_t next = B;
+            if (R != kNone) {           // (a I + B) (f I + R) - a f I = a R + f B + B R
+                next = take();
+                list.square(B, R, R, B, next, m, m, 1.0f / kGramScale, ca, f);
+                f *= ca;
+            }
+            if (more) {                 // A <- (a I + B) A (a I + B); beside the product above
+                const uint8_t T = take();
+                list.square(B, A, A, kNone, T, m, m, 1.0f / kGramScale, ca, 0.0f);
+                list.after(poly);
+                list.square(T, B, T, kNone, A, m, m, 1.0f / kGramScale, ca, 0.0f);
+                give(T);
+            }
+            if (R != kNone) {
+                give(R);
+                give(B);
+            }
+            R = next;
+        }
+        s += size;
+        // X = f X + R X
+        Phase ph = {};
+        const bool last = s == a.steps && direct;
+        const float out = last ? 1.0f / p.x_scale : 1.0f;
+        ph.a = R;
         ph.b = ph.src1 = hi;
         ph.src2 = lo;
         ph.dst = last ? static_cast<uint8_t>(kOut) : static_cast<uint8_t>(kHi0 + (x ^ 1));
         ph.dst_lo = last ? kNone : static_cast<uint8_t>(kLo0 + (x ^ 1));
         ph.result = !last ? kState : tall ? kBf16Transposed : kBf16;
-        ph.sym = false;
         ph.b_along_n = true;
         ph.n = n;
-        const float f = last ? 1.0f / p.x_scale : 1.0f;
-        ph.f_acc = f / kGramScale;
-        ph.f1 = f * a.coef[0];
+        ph.k = m;
+        ph.f_acc = out / kGramScale;
+        ph.f1 = out * f;
         ph.f2 = ph.f1 / kLoScale;
-        add(ph);
+        list.add(ph);
+        give(R);
     }
-    // Pairs of CTAs once their 256 x 256 tiles give every pair of SMs some
-    const bool pairs = Tiling<2>::units(m, run.batch, run.phases[2]) >= limits.pairs;
-    e = pairs ? launch_run<2>(run, limits.pairs, stream) : launch_run<1>(run, limits.single, stream);
+
+    // The tile that the time model below prefers
+    const double t1 = plan<1>(list, run, limits.single, l.partial_bytes, nullptr);
+    const double t2 = plan<2>(list, run, limits.pairs, l.partial_bytes, nullptr);
+    if (t2 < t1) {
+        plan<2>(list, run, limits.pairs, l.partial_bytes, &run);
+        e = launch_run<2>(run, limits.pairs, stream);
+    } else {
+        plan<1>(list, run, limits.single, l.partial_bytes, &run);
+        e = launch_run<1>(run, limits.single, stream);
+    }
     if (e != cudaSuccess || direct) return e;
     const dim3 grid(static_cast<unsigned>((l.n + 31) / 32), static_cast<unsigned>((l.m + 31) / 32),
                     static_cast<unsigned>(a.batch));
