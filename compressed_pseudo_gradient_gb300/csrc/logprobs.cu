@@ -1,19 +1,21 @@
 // Log-probabilities of given tokens with entropy and top alternatives, and their gradient
 // (spl_token_logprobs, spl_token_logprobs_grad; declared in include/spl_local.h).
 //
-// With z = scale * x over a row x of logits, m = max x, e_j = exp(scale (x_j - m)):
-//   S = sum e_j,  W = sum e_j (x_j - m)
-//   lse = scale m + log S,  logp = scale (x_t - m) - log S,  H = log S - scale W / S
+// With z = scale * x over a row x of logits, a reference m near max x, t_j = (x_j - m) scale log2 e:
+//   S = sum 2^t_j,  W = sum 2^t_j t_j
+//   lse = scale m + log S,  logp = scale (x_t - m) - log S,  H = log S - log 2 W / S
 // and with p_j = exp(z_j - lse), for upstream gradients g of logp and h of H:
 //   dx_j = scale (g (1[j = t] - p_j) - h p_j (z_j - lse + H)).
 //
 // Forward: every logit is read once.  A row goes to a cluster of CTAs (one CTA when there are
-// enough rows), each thread keeps (m, S, W) of its vectors, rescaled when its maximum rises,
-// and the triples are joined in a fixed tree (warp, CTA, cluster through distributed shared
-// memory), so a call needs no workspace and gives the same bits each run.
-// Top alternatives: each warp holds its k largest, sorted, one per lane, as 64-bit keys (the
-// value's ordered bits, then the complement of its index: equal values rank by lower index);
-// a vector is looked at again only if its maximum beats the warp's k-th entry.
+// enough rows).  A warp keeps one m for all its lanes, the largest logit it has seen, so that a
+// vote over a group of four vectors per lane almost always finds nothing to rescale; lanes keep
+// (S, W).  Warps, CTAs and the cluster's CTAs (through distributed shared memory) are joined in a
+// fixed tree, so a call needs no workspace and gives the same bits each run.
+// Top alternatives: a warp holds its k largest, sorted, one per lane, as 64-bit keys (the value's
+// ordered bits, then the complement of its index: equal values rank by lower index).  The same
+// vote tells whether a group has a value above the k-th; if so its candidates are gathered in
+// shared memory, sorted and merged.
 #include <cooperative_groups.h>
 
 #include "local_device.cuh"
@@ -25,58 +27,71 @@ namespace cg = cooperative_groups;
 namespace spl {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;
 constexpr int kMaxParts = 8;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr float kSafe = 1e30f;      // log2-domain magnitudes below this cannot overflow in a sum
+constexpr float kVanish = -1e5f;    // 2^t is 0 for certain; keeps 0 * t finite
+constexpr float kLn2 = 0.69314718056f;
+
+__device__ __forceinline__ float nan_f() { return __uint_as_float(0x7fc00000u); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
 
 // ---- the running softmax statistics ---------------------------------------------------------
 struct Stats {
-    float m;   // largest logit so far (kLowest before the first)
-    float s;   // sum of exp(scale (x - m))
-    float w;   // sum of exp(scale (x - m)) (x - m)
+    float m;   // reference (kLowest before the first value)
+    float s;   // sum of 2^t
+    float w;   // sum of 2^t t
 };
 
-// The statistics relative to another, not smaller, maximum: a vanishing factor drops them (its
-// product with w's shift may be 0 times infinity), and -inf - m is held at the lowest number.
-__device__ __forceinline__ void rescale(Stats& a, float m, float c) {
-    const float delta = fmaxf(__fsub_rn(a.m, m), kLowest);
-    const float f = ex2(__fmul_rn(delta, c));
-    a.w = f > 0.0f ? __fmul_rn(f, __fmaf_rn(a.s, delta, a.w)) : 0.0f;
-    a.s = __fmul_rn(f, a.s);
-    a.m = m;
+// The statistics relative to another, not smaller, reference.
+__device__ __forceinline__ void rescale(float m_old, float m_new, float c, float& s, float& w) {
+    const float t = fmaxf(__fmul_rn(__fsub_rn(m_old, m_new), c), kVanish);
+    const float f = ex2(t);
+    w = __fmul_rn(f, __fmaf_rn(s, t, w));
+    s = __fmul_rn(f, s);
 }
 
 __device__ __forceinline__ Stats join(Stats a, Stats b, float c) {
     const float m = max_nan(a.m, b.m);
-    rescale(a, m, c);
-    rescale(b, m, c);
-    a.s = __fadd_rn(a.s, b.s);
-    a.w = __fadd_rn(a.w, b.w);
-    return a;
+    rescale(a.m, m, c, a.s, a.w);
+    rescale(b.m, m, c, b.s, b.w);
+    return Stats{m, __fadd_rn(a.s, b.s), __fadd_rn(a.w, b.w)};
 }
 
-template <int kN>
-__device__ __forceinline__ float vector_max(const float (&x)[kN]) {
-    float v = x[0];
+__device__ __forceinline__ Stats join_warp(Stats st, float c) {
 #pragma unroll
-    for (int i = 1; i < kN; ++i) v = max_nan(v, x[i]);
-    return v;
-}
-
-// Adds kN logits with the given maximum.  A masked logit (-inf, or one so low that the
-// difference overflows) has e = 0 and adds nothing to either sum.
-template <int kN>
-__device__ __forceinline__ void add_values(Stats& a, const float (&x)[kN], float vmax, float c) {
-    if (!(vmax <= a.m)) rescale(a, max_nan(vmax, a.m), c);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        const float d = fmaxf(__fsub_rn(x[i], a.m), kLowest);
-        const float e = ex2(__fmul_rn(d, c));
-        a.s = __fadd_rn(a.s, e);
-        a.w = __fmaf_rn(e, d, a.w);
+    for (int off = 16; off > 0; off >>= 1) {
+        Stats o;
+        o.m = __shfl_xor_sync(kAll, st.m, off);
+        o.s = __shfl_xor_sync(kAll, st.s, off);
+        o.w = __shfl_xor_sync(kAll, st.w, off);
+        st = join(st, o, c);
     }
+    return st;
+}
+
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = max_nan(v, __shfl_xor_sync(kAll, v, off));
+    return v;
 }
 
 // ---- sorted lists of the largest ------------------------------------------------------------
@@ -88,8 +103,33 @@ __device__ __forceinline__ uint64_t rank_key(float x, uint32_t index) {
 
 __device__ __forceinline__ float key_value(uint64_t key) {
     const uint32_t hi = static_cast<uint32_t>(key >> 32);
-    return __uint_as_float((hi & 0x80000000u) ? (hi == 0xffffffffu ? 0x7fc00000u : hi & 0x7fffffffu)
-                                              : ~hi);
+    return (hi & 0x80000000u) ? (hi == 0xffffffffu ? nan_f() : __uint_as_float(hi & 0x7fffffffu))
+                              : __uint_as_float(~hi);
+}
+
+__device__ __forceinline__ uint64_t order_pair(uint64_t k, int off, bool larger) {
+    const uint64_t o = __shfl_xor_sync(kAll, k, off);
+    return larger == (k > o) ? k : o;
+}
+
+// Descending over the lanes (bitonic).
+__device__ __forceinline__ uint64_t sort_descending(uint64_t k, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int off = size >> 1; off > 0; off >>= 1)
+            k = order_pair(k, off, ((lane & off) == 0) == ((lane & size) == 0));
+    return k;
+}
+
+// The 32 largest of two descending lists, descending: the larger of each entry and its mirror
+// is a bitonic sequence of the 32 largest, sorted by five exchanges.
+__device__ __forceinline__ uint64_t top_merge(uint64_t a, uint64_t b, int lane) {
+    const uint64_t r = __shfl_sync(kAll, b, 31 - lane);
+    uint64_t k = a > r ? a : r;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) k = order_pair(k, off, (lane & off) == 0);
+    return k;
 }
 
 // A warp's list: lane l holds the l-th largest key so far (0: none yet).  `floor` is the value
@@ -99,56 +139,111 @@ struct TopList {
     float floor;
 };
 
-__device__ __forceinline__ void top_insert(TopList& t, uint64_t key, int lane, int k) {
-    const int at = __popc(__ballot_sync(kAll, t.key > key));
-    const uint64_t up = __shfl_up_sync(kAll, t.key, 1);
-    if (lane == at) t.key = key;
-    if (lane > at) t.key = up;
+// Merges the `count` candidates gathered in shared memory (at most 64).
+__device__ __noinline__ void top_flush(TopList& t, const uint64_t* found, int count, int lane, int k) {
+    __syncwarp();
+    for (int first = 0; first < count; first += 32) {
+        const uint64_t mine = first + lane < count ? found[first + lane] : 0;
+        t.key = top_merge(t.key, sort_descending(mine, lane), lane);
+    }
     const uint64_t last = __shfl_sync(kAll, t.key, k - 1);
-    t.floor = last == 0 ? __uint_as_float(0x7fc00000u) : key_value(last);
+    t.floor = last == 0 ? nan_f() : key_value(last);
+    __syncwarp();
 }
 
-// Offers each lane's values (indices first, first + 1, ...) to the warp's list.  Called by all
-// lanes; lanes without a vector pass ok = false.
-template <int kN>
-__device__ __noinline__ void top_offer(TopList& t, const float (&x)[kN], bool ok, uint32_t first,
-                                       int lane, int k) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        // equal values are offered too: their keys decide (vectors interleave over the lanes)
-        unsigned want = __ballot_sync(kAll, ok && !(x[i] < t.floor));
-        while (want != 0) {
-            const int src = __ffs(want) - 1;
-            const float v = __shfl_sync(kAll, x[i], src);
-            const uint32_t idx = __shfl_sync(kAll, first, src) + i;
-            top_insert(t, rank_key(v, idx), lane, k);
-            want &= want - 1;
-            want &= __ballot_sync(kAll, ok && !(x[i] < t.floor));
+// Adds a lane's value to the candidates if it may rank among the k largest.  Of equal values the
+// earlier index ranks first, and the list holds values of earlier groups only, so it takes a larger
+// one; `at_least` takes equal ones too: under the first group's bound (below), and once the list
+// has taken in values of this very group.
+__device__ __forceinline__ void top_gather(TopList& t, uint64_t* found, int& count, float x, bool ok,
+                                           bool& at_least, uint32_t index, int lane, int k) {
+    const bool want = ok && !(at_least ? x < t.floor : x <= t.floor);
+    const unsigned who = __ballot_sync(kAll, want);
+    if (who == 0) return;
+    if (count + __popc(who) > 64) {
+        const float bound = t.floor;
+        top_flush(t, found, count, lane, k);
+        if (t.floor != t.floor) t.floor = bound;
+        count = 0;
+        at_least = true;
+    }
+    if (want) found[count + __popc(who & ((1u << lane) - 1u))] = rank_key(x, index);
+    count += __popc(who);
+}
+
+// ---- one group of vectors per lane ----------------------------------------------------------
+// Four 16-byte vectors per lane.  bf16 stays packed for the extremes (two per
+// instruction) and is widened on the way into the sums.
+template <bool kBf16>
+struct Group {
+    using V = Vec16<kBf16>;
+    static constexpr int kN = V::kN, kVecs = 4;
+    uint4 raw[kVecs];
+
+    __device__ __forceinline__ float vec_max(int u) const {
+        const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+        if constexpr (kBf16) {
+            uint32_t a, b;
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w[0]), "r"(w[1]));
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w[2]), "r"(w[3]));
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+            return max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+        } else {
+            return max_nan(max_nan(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                           max_nan(__uint_as_float(w[2]), __uint_as_float(w[3])));
         }
     }
-}
-
-// The 32 largest of two descending lists, descending: the larger of each entry and its mirror
-// is a bitonic sequence of the 32 largest, sorted by five exchanges.
-__device__ __forceinline__ uint64_t top_merge(uint64_t a, uint64_t b, int lane) {
-    const uint64_t r = __shfl_sync(kAll, b, 31 - lane);
-    uint64_t k = a > r ? a : r;
+    __device__ __forceinline__ float max() const {
+        if constexpr (kBf16) {
+            uint32_t a[kVecs];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const uint64_t o = __shfl_xor_sync(kAll, k, off);
-        k = ((lane & off) == 0) == (k > o) ? k : o;
+            for (int u = 0; u < kVecs; ++u) {
+                uint32_t b;
+                asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a[u]) : "r"(raw[u].x), "r"(raw[u].y));
+                asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(raw[u].z), "r"(raw[u].w));
+                asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a[u]) : "r"(a[u]), "r"(b));
+                if (u > 0) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a[0]) : "r"(a[0]), "r"(a[u]));
+            }
+            return max_nan(__uint_as_float(a[0] << 16), __uint_as_float(a[0] & 0xffff0000u));
+        } else {
+            float v = vec_max(0);
+#pragma unroll
+            for (int u = 1; u < kVecs; ++u) v = max_nan(v, vec_max(u));
+            return v;
+        }
     }
-    return k;
-}
+    __device__ __forceinline__ float min() const {
+        if constexpr (kBf16) {
+            uint32_t a = raw[0].x;
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u) {
+                asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(raw[u].x));
+                asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(raw[u].y));
+                asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(raw[u].z));
+                asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(raw[u].w));
+            }
+            return fminf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+        } else {
+            float v = __uint_as_float(raw[0].x);
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u)
+                v = fminf(fminf(fminf(v, __uint_as_float(raw[u].x)), fminf(__uint_as_float(raw[u].y), __uint_as_float(raw[u].z))),
+                          __uint_as_float(raw[u].w));
+            return v;
+        }
+    }
+};
 
-// Bound: HBM.  Two CTAs of 512 threads per SM, four 16-byte loads in flight per thread.
+// Bound: HBM (about 5 instructions per value, one of them an exponential).
 template <bool kBf16, bool kTop>
-__global__ void __launch_bounds__(kThreads, 2) k_logprobs(const __grid_constant__ LogprobsArgs a,
+__global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) k_logprobs(const __grid_constant__ LogprobsArgs a,
                                                           int parts) {
     using V = Vec16<kBf16>;
+    using G = Group<kBf16>;
     constexpr int kN = V::kN;
     __shared__ Stats s_stats[kWarps];
     __shared__ uint64_t s_top[kTop ? kWarps : 1][32];
+    __shared__ uint64_t s_found[kTop ? kWarps : 1][64];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / parts;
     const int part = static_cast<int>(blockIdx.x % parts);
@@ -156,45 +251,117 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const __grid_constant_
         static_cast<const unsigned char*>(a.logits) + row * a.stride * V::kBytes;
     const RowSplit sp = split_row<kBf16>(base, a.vocab);
     const uint4* vecs = reinterpret_cast<const uint4*>(base + sp.head * V::kBytes);
-    const int64_t begin = sp.vecs * part / parts, end = sp.vecs * (part + 1) / parts;
+    // vectors of this part; a row has fewer than 2^31
+    const int begin = static_cast<int>(sp.vecs * part / parts), end = static_cast<int>(sp.vecs * (part + 1) / parts);
     const float c = __fmul_rn(a.scale, kLog2e);
     const float ninf = __uint_as_float(0xff800000u);
 
-    Stats st = {kLowest, 0.0f, 0.0f};
-    TopList top = {0, __uint_as_float(0x7fc00000u)};
+    float m = kLowest;                       // the warp's reference
+    float2 s2 = {0.0f, 0.0f}, w2 = {0.0f, 0.0f};
+    TopList top = {0, nan_f()};
+    bool first_group = true;
 
-    // one value per thread from index `first` on: the ends of a row around its whole vectors
+    auto load = [&](G& g, int b) {
+#pragma unroll
+        for (int u = 0; u < G::kVecs; ++u) {
+            const int v = b + u * kThreads + tid;
+            const uint32_t fill = kBf16 ? 0xff80ff80u : 0xff800000u;   // -inf
+            g.raw[u] = make_uint4(fill, fill, fill, fill);
+            if (v < end && SPL_CHECK(sp.head + (static_cast<int64_t>(v) + 1) * kN <= a.vocab, kSiteLogits, v))
+                g.raw[u] = __ldcs(vecs + v);
+        }
+    };
+    // the warp's reference rises to its largest value
+    auto raise = [&](float vmax) {
+        const float peak = warp_max_nan(max_nan(vmax, m));
+        rescale(m, peak, c, s2.x, w2.x);
+        rescale(m, peak, c, s2.y, w2.y);
+        m = peak;
+    };
+    // a value whose distance to m may be infinite adds nothing
+    auto add_guarded = [&](float x) {
+        const float t = fmaxf(__fmul_rn(__fsub_rn(x, m), c), kVanish);
+        const float e = ex2(t);
+        s2.x = __fadd_rn(s2.x, e);
+        w2.x = __fmaf_rn(e, t, w2.x);
+    };
+    // one value per lane of warp 0 from index `first` on: the ends of a row around its vectors
     auto scalars = [&](int64_t first, int count) {
-        const bool ok = tid < count && SPL_CHECK(first + tid < a.vocab, kSiteLogits, first + tid);
-        const float x[1] = {ok ? V::load1(base, first + tid) : ninf};
-        if (ok) add_values<1>(st, x, x[0], c);
-        if constexpr (kTop)
-            if (warp == 0) top_offer<1>(top, x, ok, static_cast<uint32_t>(first + tid), lane, a.top);
+        if (warp != 0) return;
+        const bool ok = lane < count && SPL_CHECK(first + lane < a.vocab, kSiteLogits, first + lane);
+        const float x = ok ? V::load1(base, first + lane) : ninf;
+        if (__any_sync(kAll, !(x <= m))) raise(x);
+        if (ok) add_guarded(x);
+        if constexpr (kTop) {
+            int count_found = 0;
+            bool at_least = false;
+            top_gather(top, s_found[0], count_found, x, ok, at_least, static_cast<uint32_t>(first + lane), lane, a.top);
+            if (count_found > 0) top_flush(top, s_found[0], count_found, lane, a.top);
+        }
     };
 
     if (part == 0 && sp.head > 0) scalars(0, sp.head);
-    for (int64_t b = begin; b < end; b += kThreads * kUnroll) {
-        uint4 raw[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t v = b + u * kThreads + tid;
-            const uint32_t fill = kBf16 ? 0xff80ff80u : 0xff800000u;   // -inf
-            raw[u] = make_uint4(fill, fill, fill, fill);
-            if (v < end && SPL_CHECK(sp.head + (v + 1) * kN <= a.vocab, kSiteLogits, v))
-                raw[u] = __ldcs(vecs + v);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float x[kN];
-            V::unpack(raw[u], x);
-            const float vmax = vector_max(x);
+    G next;
+    load(next, begin);
+    for (int b = begin; b < end; b += kThreads * G::kVecs) {
+        const G g = next;
+        load(next, b + kThreads * G::kVecs);   // past the end: nothing is read
+        const float vmax = g.max();
+        const bool guarded = !(__fmul_rn(g.min(), c) > -kSafe);
+        bool look = guarded || !(vmax <= m);
+        if constexpr (kTop) look |= !(vmax <= top.floor);
+        if (__any_sync(kAll, look)) {
+            if (__any_sync(kAll, !(vmax <= m))) raise(vmax);
             if constexpr (kTop) {
-                const int64_t v = b + u * kThreads + tid;
-                const bool ok = v < end;
-                if (__any_sync(kAll, ok && !(vmax <= top.floor)))
-                    top_offer<kN>(top, x, ok, static_cast<uint32_t>(sp.head + v * kN), lane, a.top);
+                if (__any_sync(kAll, !(vmax <= top.floor))) {
+                    bool at_least = false;
+                    if (first_group && top.floor != top.floor) {
+                        // k of the lanes' largest are at least the k-th of them
+                        const uint64_t k = sort_descending(rank_key(vmax, 0), lane);
+                        at_least = true;
+                        top.floor = key_value(__shfl_sync(kAll, k, a.top - 1));
+                    }
+                    int count = 0;
+#pragma unroll
+                    for (int u = 0; u < G::kVecs; ++u) {
+                        const int v = b + u * kThreads + tid;
+                        const float um = g.vec_max(u);
+                        if (!__any_sync(kAll, at_least ? !(um < top.floor) : !(um <= top.floor))) continue;
+                        float x[kN];
+                        V::unpack(g.raw[u], x);
+#pragma unroll
+                        for (int i = 0; i < kN; ++i)
+                            top_gather(top, s_found[warp], count, x[i], v < end, at_least,
+                                       static_cast<uint32_t>(sp.head + v * kN + i), lane, a.top);
+                    }
+                    top_flush(top, s_found[warp], count, lane, a.top);
+                }
+                first_group = false;
             }
-            add_values<kN>(st, x, vmax, c);
+        }
+        const float mc = __fmul_rn(m, c);
+        if (__any_sync(kAll, guarded) || !(fabsf(mc) < kSafe)) {
+#pragma unroll
+            for (int u = 0; u < G::kVecs; ++u) {
+                float x[kN];
+                V::unpack(g.raw[u], x);
+#pragma unroll
+                for (int i = 0; i < kN; ++i) add_guarded(x[i]);
+            }
+        } else {
+            const float2 c2 = {c, c}, mc2 = {-mc, -mc};
+#pragma unroll
+            for (int u = 0; u < G::kVecs; ++u) {
+                float x[kN];
+                V::unpack(g.raw[u], x);
+#pragma unroll
+                for (int i = 0; i < kN; i += 2) {
+                    const float2 t = fma2(make_float2(x[i], x[i + 1]), c2, mc2);
+                    const float2 e = {ex2(t.x), ex2(t.y)};
+                    s2 = add2(s2, e);
+                    w2 = fma2(e, t, w2);
+                }
+            }
         }
     }
     if (part == parts - 1) {
@@ -202,14 +369,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const __grid_constant_
         if (done < a.vocab) scalars(done, static_cast<int>(a.vocab - done));
     }
 
-    // join: warp, CTA
+    // join: lanes (one reference), the CTA's warps
+    Stats st = {m, __fadd_rn(s2.x, s2.y), __fadd_rn(w2.x, w2.y)};
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
-        Stats o;
-        o.m = __shfl_xor_sync(kAll, st.m, off);
-        o.s = __shfl_xor_sync(kAll, st.s, off);
-        o.w = __shfl_xor_sync(kAll, st.w, off);
-        st = join(st, o, c);
+        st.s = __fadd_rn(st.s, __shfl_xor_sync(kAll, st.s, off));
+        st.w = __fadd_rn(st.w, __shfl_xor_sync(kAll, st.w, off));
     }
     if (lane == 0) s_stats[warp] = st;
     if constexpr (kTop) s_top[warp][lane] = top.key;
@@ -220,37 +385,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const __grid_constant_
             __syncthreads();
         }
     }
-    if (warp == 0) {
-        st = lane < kWarps ? s_stats[lane] : Stats{kLowest, 0.0f, 0.0f};
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            Stats o;
-            o.m = __shfl_xor_sync(kAll, st.m, off);
-            o.s = __shfl_xor_sync(kAll, st.s, off);
-            o.w = __shfl_xor_sync(kAll, st.w, off);
-            st = join(st, o, c);
-        }
-    }
-    if (parts > 1) {   // join the cluster's CTAs in the first one
+    const Stats none = {kLowest, 0.0f, 0.0f};
+    if (warp == 0) st = join_warp(lane < kWarps ? s_stats[lane] : none, c);
+    if (parts > 1) {   // the cluster's CTAs, in the first one
         cg::cluster_group cluster = cg::this_cluster();
+        __syncwarp();
         if (tid == 0) s_stats[0] = st;
         cluster.sync();
-        if (part == 0 && warp == 0) {
-            st = Stats{kLowest, 0.0f, 0.0f};
-            if (lane < parts) st = *cluster.map_shared_rank(&s_stats[0], lane);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-                Stats o;
-                o.m = __shfl_xor_sync(kAll, st.m, off);
-                o.s = __shfl_xor_sync(kAll, st.s, off);
-                o.w = __shfl_xor_sync(kAll, st.w, off);
-                st = join(st, o, c);
-            }
+        if (part == 0) {
+            if (warp == 0) st = join_warp(lane < parts ? *cluster.map_shared_rank(&s_stats[0], lane) : none, c);
             if constexpr (kTop) {
-                uint64_t k = s_top[0][lane];
-                for (int p = 1; p < parts; ++p)
-                    k = top_merge(k, *cluster.map_shared_rank(&s_top[0][lane], p), lane);
-                s_top[0][lane] = k;
+                // warp q takes the lists of the parts q and q + kWarps
+                uint64_t k = 0;
+                for (int q = warp; q < parts; q += kWarps)
+                    k = top_merge(k, *cluster.map_shared_rank(&s_top[0][lane], q), lane);
+                __syncthreads();
+                s_top[warp][lane] = k;
+                __syncthreads();
+                for (int half = kWarps / 2; half > 0; half >>= 1) {
+                    if (warp < half)
+                        s_top[warp][lane] = top_merge(s_top[warp][lane], s_top[warp + half][lane], lane);
+                    __syncthreads();
+                }
             }
         }
         cluster.sync();   // the other CTAs' shared memory has been read
@@ -259,26 +415,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const __grid_constant_
 
     const bool broken = !(fabsf(st.m) <= 3.402823466e+38f);   // NaN or infinite maximum
     const bool empty = !broken && st.s == 0.0f;               // every logit is -inf
-    const float nan = __uint_as_float(0x7fc00000u);
-    const float peak = __fmul_rn(st.m, a.scale);
     const float log_s = logf(st.s);
     auto logprob = [&](float x) {
-        if (broken) return nan;
+        if (broken) return nan_f();
         if (empty) return ninf;
         return __fsub_rn(__fmul_rn(__fsub_rn(x, st.m), a.scale), log_s);
     };
     if (lane == 0) {
         if (a.lse != nullptr)
-            a.lse[row] = broken ? nan : empty ? ninf : __fadd_rn(peak, log_s);
+            a.lse[row] = broken ? nan_f() : empty ? ninf : __fmaf_rn(st.m, a.scale, log_s);
         if (a.entropy != nullptr)
-            a.entropy[row] = broken ? nan
+            a.entropy[row] = broken ? nan_f()
                              : empty ? 0.0f
-                                     : __fsub_rn(log_s, __fdiv_rn(__fmul_rn(a.scale, st.w), st.s));
+                                     : __fsub_rn(log_s, __fmul_rn(kLn2, __fdiv_rn(st.w, st.s)));
         if (a.targets.data != nullptr) {
             const int64_t t = token_at(a.targets, row);
             float lp = 0.0f;   // a negative target is outside the loss
             if (t >= a.vocab) {
-                lp = nan;
+                lp = nan_f();
                 if (a.flags != nullptr) atomicOr(a.flags, kFlagBadToken);
             } else if (t >= 0 && SPL_CHECK(t < a.vocab, kSiteLogits, t)) {
                 lp = logprob(V::load1(base, t));
@@ -400,7 +554,7 @@ cudaError_t launch_forward(const LogprobsArgs& a, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     int parts = 1;
-    while (parts < kMaxParts && a.rows * parts < 2 * sms && a.vocab / (2 * parts) >= 2048) parts *= 2;
+    while (parts < kMaxParts && a.rows * parts < 4 * sms && a.vocab / (2 * parts) >= 2048) parts *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows * parts));
     cfg.blockDim = dim3(kThreads);

@@ -36,7 +36,7 @@ constexpr float kLoScale = 2048.0f;      // of the state's low plane
 
 // ---- momentum, norm, state ------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
-constexpr int kMaxPartials = 512;   // sums of squares per matrix
+constexpr int kMaxPartials = 1216;  // sums of squares per matrix: eight CTAs per SM
 constexpr int kMaxPhases = 160;     // of the run kernel below
 
 struct PrepArgs {
@@ -238,32 +238,36 @@ __global__ void __launch_bounds__(kPrepThreads) k_orth_state_tall(const __grid_c
     using U = PrepUnit<kBf16, kVec>;
     constexpr int kAcross = 64 / U::kN, kDown = kPrepThreads / kAcross;
     __shared__ float s_tile[64][65];
-    const int64_t b = blockIdx.z;
+    const int64_t b = blockIdx.y;
     const float f = state_factor(p, b);
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64, c0 = static_cast<int64_t>(blockIdx.y) * 64;
+    const int64_t tiles_r = (p.rows + 63) / 64, tiles = tiles_r * ((p.cols + 63) / 64);
     const int uc = threadIdx.x % kAcross, ur = threadIdx.x / kAcross;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t r0 = t % tiles_r * 64, c0 = t / tiles_r * 64;
 #pragma unroll
-    for (int k = 0; k < 64 / kDown; ++k) {
-        const int64_t r = r0 + ur + k * kDown, c = c0 + uc * U::kN;
-        if (r >= p.rows || c >= p.cols || !SPL_CHECK(r < p.rows, kSiteOrthIn, r)) continue;
-        U g, m;
-        g.load(p, b, r, c / U::kN);
-        if (p.momentum != nullptr) m.load_momentum(p.momentum + (b * p.rows + r) * p.cols + c);
+        for (int k = 0; k < 64 / kDown; ++k) {
+            const int64_t r = r0 + ur + k * kDown, c = c0 + uc * U::kN;
+            if (r >= p.rows || c >= p.cols || !SPL_CHECK(r < p.rows, kSiteOrthIn, r)) continue;
+            U g, m;
+            g.load(p, b, r, c / U::kN);
+            if (p.momentum != nullptr) m.load_momentum(p.momentum + (b * p.rows + r) * p.cols + c);
 #pragma unroll
-        for (int i = 0; i < U::kN; ++i)
-            s_tile[ur + k * kDown][uc * U::kN + i] = __fmul_rn(step_value(g.x[i], m.x[i], p), f);
-    }
-    __syncthreads();
+            for (int i = 0; i < U::kN; ++i)
+                s_tile[ur + k * kDown][uc * U::kN + i] = __fmul_rn(step_value(g.x[i], m.x[i], p), f);
+        }
+        __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {   // 8 of the tile's rows per thread: the state's columns
-        const int c = (threadIdx.x >> 3) + 32 * k, r = (threadIdx.x & 7) * 8;
-        if (c0 + c >= p.cols || r0 + r >= p.rows) continue;
-        // columns up to the row pitch, a multiple of 8, are this buffer's own
-        if (!SPL_CHECK(r0 + r + 8 <= p.ld, kSiteOrthState, r0 + r)) continue;
-        float x[8];
+        for (int k = 0; k < 2; ++k) {   // 8 of the tile's rows per thread: the state's columns
+            const int c = (threadIdx.x >> 3) + 32 * k, r = (threadIdx.x & 7) * 8;
+            if (c0 + c >= p.cols || r0 + r >= p.rows) continue;
+            // columns up to the row pitch, a multiple of 8, are this buffer's own
+            if (!SPL_CHECK(r0 + r + 8 <= p.ld, kSiteOrthState, r0 + r)) continue;
+            float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = s_tile[r + i][c];
-        store_state<8>(p, b * p.plane + (c0 + c) * p.ld + r0 + r, x);
+            for (int i = 0; i < 8; ++i) x[i] = s_tile[r + i][c];
+            store_state<8>(p, b * p.plane + (c0 + c) * p.ld + r0 + r, x);
+        }
+        __syncthreads();
     }
 }
 
@@ -274,11 +278,12 @@ cudaError_t launch_prep(PrepArgs p, int64_t batch, bool tall, int sms, cudaStrea
     p.num_partials = static_cast<int>(ctas < kMaxPartials ? ctas : kMaxPartials);
     const unsigned b = static_cast<unsigned>(batch);
     k_orth_norm<kBf16, kVec><<<dim3(static_cast<unsigned>(p.num_partials), b), kPrepThreads, 0, stream>>>(p);
+    const int64_t most = 8 * static_cast<int64_t>(sms);   // as many as are resident, then loop
     if (tall) {
-        const dim3 grid(static_cast<unsigned>((p.rows + 63) / 64), static_cast<unsigned>((p.cols + 63) / 64), b);
-        k_orth_state_tall<kBf16, kVec><<<grid, kPrepThreads, 0, stream>>>(p);
+        const int64_t tiles = (p.rows + 63) / 64 * ((p.cols + 63) / 64);
+        k_orth_state_tall<kBf16, kVec><<<dim3(static_cast<unsigned>(tiles < most ? tiles : most), b), kPrepThreads,
+                                         0, stream>>>(p);
     } else {
-        const int64_t most = 16 * static_cast<int64_t>(sms);   // a few waves, then loop
         k_orth_state<kBf16, kVec><<<dim3(static_cast<unsigned>(ctas < most ? ctas : most), b), kPrepThreads, 0,
                                     stream>>>(p);
     }
