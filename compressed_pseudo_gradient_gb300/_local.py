@@ -8,7 +8,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._binding import _BF16, _F32, _check, _flags_ptr, _stream, library
+from ._binding import _BF16, _F32, _check, _flags_ptr, library
 
 MAX_TOP = 32
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)   # the usual coefficients for 5 steps
@@ -26,15 +26,29 @@ class TokenLogprobs(NamedTuple):
 
 
 def _cuda(t, name, dtypes, dev=None):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    try:
+        if t.is_cuda and t.dtype in dtypes and (dev is None or t.device == dev):
+            return t
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}; expected one of {dtypes}")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    return t
+    raise ValueError(f"{name} must be on {dev}")
+
+
+def _call(fn, dev, *args):
+    """The library call with the device's current stream as its last argument.  The calls are
+    small enough for the host's share to show: the device is switched only if it has to be."""
+    index = dev.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != 0:
+        _check(fn.__name__, st)
 
 
 def _rows(t, name):
@@ -42,23 +56,23 @@ def _rows(t, name):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    stride, inner = t.stride()
+    if cols > 1 and inner != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    if rows > 1 and t.stride(0) < cols:
+    if rows > 1 and stride < cols:
         raise ValueError(f"the rows of {name} must not overlap")
-    return t.stride(0) if rows > 1 else cols
+    return stride if rows > 1 else cols
 
 
 def _vector(t, name, n, dtypes, dev):
     _cuda(t, name, dtypes, dev)
     if not t.is_contiguous() or t.numel() != n:
         raise ValueError(f"{name} must hold {n} contiguous values")
-    return t
+    return t.data_ptr()
 
 
 def _ids(t, name, n, dev):
-    t = _vector(t, name, n, _IDS, dev)
-    return t.data_ptr(), 64 if t.dtype == torch.int64 else 32
+    return _vector(t, name, n, _IDS, dev), 64 if t.dtype == torch.int64 else 32
 
 
 def _dt(t):
@@ -88,20 +102,17 @@ def token_logprobs(logits, targets=None, *, scale: float = 1.0, top: int = 0,
     rows, vocab = logits.shape
     dev, top = logits.device, int(top)
     ids, bits = (None, 64) if targets is None else _ids(targets, "targets", rows, dev)
-    stats = torch.empty((3, rows), dtype=torch.float32, device=dev)
-    top_ids = top_logp = None
+    logp, lse, entropy = torch.empty((3, rows), dtype=torch.float32, device=dev).unbind(0)
+    base = lse.data_ptr() - 4 * rows
+    top_ids = top_logp = id_out = logp_out = None
     if top > 0:
         top_ids = torch.empty((rows, top), dtype=torch.int64, device=dev)
         top_logp = torch.empty((rows, top), dtype=torch.float32, device=dev)
-    base, step = stats.data_ptr(), 4 * rows
-    with torch.cuda.device(dev):
-        st = lib.spl_token_logprobs(logits.data_ptr(), _dt(logits), rows, vocab, stride, ids, bits,
-                                    float(scale), top, None if ids is None else base, base + step,
-                                    base + 2 * step, None if top_ids is None else top_ids.data_ptr(),
-                                    None if top_logp is None else top_logp.data_ptr(),
-                                    _flags_ptr(flags, dev), _stream(dev))
-    _check("spl_token_logprobs", st)
-    return TokenLogprobs(None if ids is None else stats[0], stats[1], stats[2], top_ids, top_logp)
+        id_out, logp_out = top_ids.data_ptr(), top_logp.data_ptr()
+    _call(lib.spl_token_logprobs, dev, logits.data_ptr(), _dt(logits), rows, vocab, stride, ids,
+          bits, scale, top, None if ids is None else base, base + 4 * rows, base + 8 * rows, id_out,
+          logp_out, _flags_ptr(flags, dev))
+    return TokenLogprobs(None if ids is None else logp, lse, entropy, top_ids, top_logp)
 
 
 def token_logprobs_grad(logits, targets, lse, d_logp, *, entropy=None, d_entropy=None,
@@ -115,30 +126,28 @@ def token_logprobs_grad(logits, targets, lse, d_logp, *, entropy=None, d_entropy
     stride = _rows(logits, "logits")
     rows, vocab = logits.shape
     dev, f32 = logits.device, (torch.float32,)
-    ids, bits = (None, 64) if targets is None else _ids(targets, "targets", rows, dev)
-    _vector(lse, "lse", rows, f32, dev)
     if (targets is None) != (d_logp is None):
         raise ValueError("targets and d_logp go together")
-    if d_logp is not None:
-        _vector(d_logp, "d_logp", rows, f32, dev)
+    ids, bits, gp, hp, ep = None, 64, None, None, None
+    if targets is not None:
+        ids, bits = _ids(targets, "targets", rows, dev)
+        gp = _vector(d_logp, "d_logp", rows, f32, dev)
     if d_entropy is not None:
-        _vector(d_entropy, "d_entropy", rows, f32, dev)
         if entropy is None:
             raise ValueError("d_entropy needs the forward call's entropy")
-        _vector(entropy, "entropy", rows, f32, dev)
+        hp = _vector(d_entropy, "d_entropy", rows, f32, dev)
+        ep = _vector(entropy, "entropy", rows, f32, dev)
     if out is None:   # rows as far apart as the logits': both then move in whole vectors
         out = torch.empty((rows, stride), dtype=logits.dtype, device=dev)[:, :vocab] \
-            if rows and vocab <= stride <= vocab + 64 else torch.empty_like(logits)
-    _cuda(out, "out", (logits.dtype,), dev)
-    if out.shape != logits.shape:
-        raise ValueError("out must have the logits' shape")
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    with torch.cuda.device(dev):
-        st = lib.spl_token_logprobs_grad(logits.data_ptr(), _dt(logits), rows, vocab, stride, ids,
-                                         bits, float(scale), lse.data_ptr(), ptr(d_logp),
-                                         ptr(entropy), ptr(d_entropy), out.data_ptr(),
-                                         _rows(out, "out"), _flags_ptr(flags, dev), _stream(dev))
-    _check("spl_token_logprobs_grad", st)
+            if rows and vocab < stride <= vocab + 64 else \
+            torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
+    else:
+        _cuda(out, "out", (logits.dtype,), dev)
+        if out.shape != logits.shape:
+            raise ValueError("out must have the logits' shape")
+    _call(lib.spl_token_logprobs_grad, dev, logits.data_ptr(), _dt(logits), rows, vocab, stride,
+          ids, bits, scale, _vector(lse, "lse", rows, f32, dev), gp, ep, hp, out.data_ptr(),
+          _rows(out, "out"), _flags_ptr(flags, dev))
     return out
 
 
@@ -154,17 +163,17 @@ def embedding(ids, table, *, scale: float = 1.0, out=None, flags=None):
     _cuda(ids, "ids", _IDS, dev)
     n = ids.numel()
     id_ptr, bits = _ids(ids, "ids", n, dev)
+    out_stride = width
     if out is None:
         out = torch.empty((*ids.shape, width), dtype=table.dtype, device=dev)
-    _cuda(out, "out", (table.dtype,), dev)
-    if out.shape != (*ids.shape, width) or (out.dim() != 2 and not out.is_contiguous()):
-        raise ValueError("out must be [*ids.shape, width] (contiguous unless 2-D)")
-    out_stride = _rows(out, "out") if out.dim() == 2 else width
-    with torch.cuda.device(dev):
-        st = lib.spl_embedding(id_ptr, bits, n, table.data_ptr(), _dt(table), vocab, width, stride,
-                               float(scale), out.data_ptr(), out_stride, _flags_ptr(flags, dev),
-                               _stream(dev))
-    _check("spl_embedding", st)
+    else:
+        _cuda(out, "out", (table.dtype,), dev)
+        if out.shape != (*ids.shape, width) or (out.dim() != 2 and not out.is_contiguous()):
+            raise ValueError("out must be [*ids.shape, width] (contiguous unless 2-D)")
+        if out.dim() == 2:
+            out_stride = _rows(out, "out")
+    _call(lib.spl_embedding, dev, id_ptr, bits, n, table.data_ptr(), _dt(table), vocab, width,
+          stride, scale, out.data_ptr(), out_stride, _flags_ptr(flags, dev))
     return out
 
 
@@ -175,7 +184,7 @@ def embedding_grad(ids, d_out, vocab: int, *, scale: float = 1.0, padding_id: in
 
     d_out: fp32 or bf16 [*ids.shape, width], rows contiguous.  With ``accumulate`` the sums are
     added to ``out`` (which must then be given); otherwise every row is written.  Tokens equal to
-    padding_id take no part."""
+    padding_id take no part.  ``workspace`` (uint8) may be kept between calls on one stream."""
     lib = library()
     _cuda(d_out, "d_out", _DENSE)
     dev = d_out.device
@@ -188,22 +197,21 @@ def embedding_grad(ids, d_out, vocab: int, *, scale: float = 1.0, padding_id: in
             raise ValueError("d_out must be contiguous unless 2-D")
         d_out = d_out.reshape(n, width)
     id_ptr, bits = _ids(ids, "ids", n, dev)
+    vocab, out_stride = int(vocab), width
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         out = torch.empty((vocab, width), dtype=torch.float32, device=dev)
-    _cuda(out, "out", (torch.float32,), dev)
-    if out.shape != (vocab, width):
-        raise ValueError("out must be [vocab, width]")
-    need = lib.spl_embedding_grad_workspace(n, int(vocab), width)
+    else:
+        _cuda(out, "out", (torch.float32,), dev)
+        if out.shape != (vocab, width):
+            raise ValueError("out must be [vocab, width]")
+        out_stride = _rows(out, "out")
+    need = lib.spl_embedding_grad_workspace(n, vocab, width)
     workspace = _workspace(workspace, need, dev)
-    with torch.cuda.device(dev):
-        st = lib.spl_embedding_grad(id_ptr, bits, n, d_out.data_ptr(), _dt(d_out), width,
-                                    _rows(d_out, "d_out"), int(vocab), float(scale),
-                                    int(padding_id), int(bool(accumulate)), out.data_ptr(),
-                                    _rows(out, "out"), workspace.data_ptr(), workspace.numel(),
-                                    _flags_ptr(flags, dev), _stream(dev))
-    _check("spl_embedding_grad", st)
+    _call(lib.spl_embedding_grad, dev, id_ptr, bits, n, d_out.data_ptr(), _dt(d_out), width,
+          _rows(d_out, "d_out"), vocab, scale, padding_id, int(bool(accumulate)), out.data_ptr(),
+          out_stride, workspace.data_ptr(), need, _flags_ptr(flags, dev))
     return out
 
 
@@ -228,30 +236,35 @@ def orthogonalize(update, *, momentum=None, mu: float = 0.95, nesterov: bool = T
     if update.dim() not in (2, 3) or update.numel() == 0:
         raise ValueError("update must be a non-empty matrix or stack of matrices")
     dev = update.device
-    u = update if update.dim() == 3 else update.unsqueeze(0)
-    batch, rows, cols = u.shape
-    if cols > 1 and u.stride(2) != 1:
+    shape, strides = update.shape, update.stride()
+    if len(shape) == 2:
+        (batch, rows, cols), (batch_stride, row_stride, inner) = (1, *shape), (0, *strides)
+    else:
+        (batch, rows, cols), (batch_stride, row_stride, inner) = shape, strides
+    if cols > 1 and inner != 1:
         raise ValueError("the rows of update must be contiguous")
-    row_stride = u.stride(1) if rows > 1 else cols
-    batch_stride = u.stride(0) if batch > 1 else rows * row_stride
-    if row_stride < cols or (batch > 1 and batch_stride < (rows - 1) * row_stride + cols):
+    if rows == 1:
+        row_stride = cols
+    if batch == 1:
+        batch_stride = rows * row_stride
+    if row_stride < cols or batch_stride < (rows - 1) * row_stride + cols:
         raise ValueError("the rows and matrices of update must not overlap")
+    mom = None
     if momentum is not None:
         _cuda(momentum, "momentum", (torch.float32,), dev)
-        if momentum.shape != update.shape or not momentum.is_contiguous():
+        if momentum.shape != shape or not momentum.is_contiguous():
             raise ValueError("momentum must be contiguous, of the update's shape")
+        mom = momentum.data_ptr()
     if out is None:
-        out = torch.empty(update.shape, dtype=torch.bfloat16, device=dev)
-    _cuda(out, "out", (torch.bfloat16,), dev)
-    if out.shape != update.shape or not out.is_contiguous():
-        raise ValueError("out must be contiguous, of the update's shape")
-    workspace = _workspace(workspace, lib.spl_orthogonalize_workspace(batch, rows, cols), dev)
-    coef = (ctypes.c_float * 3)(*[float(c) for c in coefficients])
-    with torch.cuda.device(dev):
-        st = lib.spl_orthogonalize(update.data_ptr(), _dt(update), batch, rows, cols, row_stride,
-                                   batch_stride, None if momentum is None else momentum.data_ptr(),
-                                   float(mu), int(bool(nesterov)), int(steps), coef, float(eps),
-                                   out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                   _flags_ptr(flags, dev), _stream(dev))
-    _check("spl_orthogonalize", st)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _cuda(out, "out", (torch.bfloat16,), dev)
+        if out.shape != shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of the update's shape")
+    need = lib.spl_orthogonalize_workspace(batch, rows, cols)
+    workspace = _workspace(workspace, need, dev)
+    _call(lib.spl_orthogonalize, dev, update.data_ptr(), _dt(update), batch, rows, cols,
+          row_stride, batch_stride, mom, mu, int(bool(nesterov)), steps,
+          (ctypes.c_float * 3)(*coefficients), eps, out.data_ptr(), workspace.data_ptr(), need,
+          _flags_ptr(flags, dev))
     return out

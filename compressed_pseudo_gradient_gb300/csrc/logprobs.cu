@@ -12,10 +12,13 @@
 // vote over a group of four vectors per lane almost always finds nothing to rescale; lanes keep
 // (S, W).  Warps, CTAs and the cluster's CTAs (through distributed shared memory) are joined in a
 // fixed tree, so a call needs no workspace and gives the same bits each run.
-// Top alternatives: a warp holds its k largest, sorted, one per lane, as 64-bit keys (the value's
-// ordered bits, then the complement of its index: equal values rank by lower index).  The same
-// vote tells whether a group has a value above the k-th; if so its candidates are gathered in
-// shared memory, sorted and merged.
+// Top alternatives: the pass over the row only notes, per thread, the largest value of each
+// segment of it.  The k-th largest of the threads' maxima is a lower bound of the row's k-th
+// value, so only the few segments that reach it are read again (from L2) for the candidates,
+// which are ranked as 64-bit keys (the value's ordered bits, then the complement of its index:
+// equal values rank by lower index), sorted and merged 32 at a time in a warp's lanes.  A row with
+// too many values at the bound (ties, few unmasked values) is read again in full instead.
+// 4096 x 262,208 bf16 with 5 alternatives: LISTTIME; 0.308 ms with none.
 #include <cooperative_groups.h>
 
 #include "local_device.cuh"
@@ -29,7 +32,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxParts = 8;
+constexpr int kMaxParts = 16;
+constexpr int kMaxSegs = 36;             // segments per thread whose maxima are kept
+constexpr int kMaxFound = kWarps * 64;   // segments, and candidates, that are listed
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kSafe = 1e30f;      // log2-domain magnitudes below this cannot overflow in a sum
 constexpr float kVanish = -1e5f;    // 2^t is 0 for certain; keeps 0 * t finite
@@ -139,7 +144,15 @@ struct TopList {
     float floor;
 };
 
-// Merges the `count` candidates gathered in shared memory (at most 64).
+// The warps' lists into the first one's, in a fixed tree.
+__device__ __forceinline__ void merge_warps(uint64_t (*lists)[32], int warp, int lane) {
+    for (int half = kWarps / 2; half > 0; half >>= 1) {
+        if (warp < half) lists[warp][lane] = top_merge(lists[warp][lane], lists[warp + half][lane], lane);
+        __syncthreads();
+    }
+}
+
+// Merges the `count` candidates gathered in shared memory.
 __device__ __noinline__ void top_flush(TopList& t, const uint64_t* found, int count, int lane, int k) {
     __syncwarp();
     for (int first = 0; first < count; first += 32) {
@@ -151,24 +164,29 @@ __device__ __noinline__ void top_flush(TopList& t, const uint64_t* found, int co
     __syncwarp();
 }
 
-// Adds a lane's value to the candidates if it may rank among the k largest.  Of equal values the
-// earlier index ranks first, and the list holds values of earlier groups only, so it takes a larger
-// one; `at_least` takes equal ones too: under the first group's bound (below), and once the list
-// has taken in values of this very group.
+// Adds a lane's value to the (at most 64) candidates of its warp if it may rank among the k
+// largest.  Of equal values the earlier index ranks first, and the list holds values of earlier
+// vectors only, so it takes a larger one; `at_least` takes equal ones too: once the list has taken
+// in values of this very vector.
 __device__ __forceinline__ void top_gather(TopList& t, uint64_t* found, int& count, float x, bool ok,
-                                           bool& at_least, uint32_t index, int lane, int k) {
+                                           bool at_least, uint32_t index, int lane, int k) {
     const bool want = ok && !(at_least ? x < t.floor : x <= t.floor);
     const unsigned who = __ballot_sync(kAll, want);
     if (who == 0) return;
     if (count + __popc(who) > 64) {
-        const float bound = t.floor;
         top_flush(t, found, count, lane, k);
-        if (t.floor != t.floor) t.floor = bound;
         count = 0;
-        at_least = true;
     }
     if (want) found[count + __popc(who & ((1u << lane) - 1u))] = rank_key(x, index);
     count += __popc(who);
+}
+
+template <int kN>
+__device__ __forceinline__ float vector_max(const float (&x)[kN]) {
+    float v = x[0];
+#pragma unroll
+    for (int i = 1; i < kN; ++i) v = max_nan(v, x[i]);
+    return v;
 }
 
 // ---- one group of vectors per lane ----------------------------------------------------------
@@ -236,14 +254,17 @@ struct Group {
 
 // Bound: HBM (about 5 instructions per value, one of them an exponential).
 template <bool kBf16, bool kTop>
-__global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) k_logprobs(const __grid_constant__ LogprobsArgs a,
+__global__ void __launch_bounds__(kThreads, 4) k_logprobs(const __grid_constant__ LogprobsArgs a,
                                                           int parts) {
     using V = Vec16<kBf16>;
     using G = Group<kBf16>;
     constexpr int kN = V::kN;
     __shared__ Stats s_stats[kWarps];
     __shared__ uint64_t s_top[kTop ? kWarps : 1][32];
-    __shared__ uint64_t s_found[kTop ? kWarps : 1][64];
+    __shared__ uint64_t s_found[kTop ? kMaxFound : 1];
+    __shared__ float s_seg[kTop ? kMaxSegs : 1][kTop ? kThreads : 1];
+    __shared__ uint32_t s_list[kTop ? kMaxFound : 1];
+    __shared__ uint32_t s_segs_found, s_found_total;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / parts;
     const int part = static_cast<int>(blockIdx.x % parts);
@@ -258,8 +279,11 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) k_logprobs(const __gri
 
     float m = kLowest;                       // the warp's reference
     float2 s2 = {0.0f, 0.0f}, w2 = {0.0f, 0.0f};
-    TopList top = {0, nan_f()};
-    bool first_group = true;
+    float lane_max = ninf, seg_max = ninf;   // of the thread's vectors, and of its current segment
+    // a segment of a thread: the fewest groups that keep it to kMaxSegs of them
+    constexpr int kGroup = kThreads * G::kVecs;
+    const int groups = (end - begin + kGroup - 1) / kGroup, seg_groups = (groups + kMaxSegs - 1) / kMaxSegs;
+    int seg = 0, in_seg = 0;
 
     auto load = [&](G& g, int b) {
 #pragma unroll
@@ -268,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) k_logprobs(const __gri
             const uint32_t fill = kBf16 ? 0xff80ff80u : 0xff800000u;   // -inf
             g.raw[u] = make_uint4(fill, fill, fill, fill);
             if (v < end && SPL_CHECK(sp.head + (static_cast<int64_t>(v) + 1) * kN <= a.vocab, kSiteLogits, v))
-                g.raw[u] = __ldcs(vecs + v);
+                g.raw[u] = kTop ? __ldcg(vecs + v) : __ldcs(vecs + v);
         }
     };
     // the warp's reference rises to its largest value
@@ -292,55 +316,34 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) k_logprobs(const __gri
         const float x = ok ? V::load1(base, first + lane) : ninf;
         if (__any_sync(kAll, !(x <= m))) raise(x);
         if (ok) add_guarded(x);
-        if constexpr (kTop) {
-            int count_found = 0;
-            bool at_least = false;
-            top_gather(top, s_found[0], count_found, x, ok, at_least, static_cast<uint32_t>(first + lane), lane, a.top);
-            if (count_found > 0) top_flush(top, s_found[0], count_found, lane, a.top);
-        }
     };
+    const int64_t done = sp.head + sp.vecs * kN;
+    const int head = part == 0 ? sp.head : 0, tail = part == parts - 1 ? static_cast<int>(a.vocab - done) : 0;
 
-    if (part == 0 && sp.head > 0) scalars(0, sp.head);
+    if (head > 0) scalars(0, head);
     G next;
     load(next, begin);
-    for (int b = begin; b < end; b += kThreads * G::kVecs) {
+    for (int b = begin; b < end; b += kGroup) {
         const G g = next;
-        load(next, b + kThreads * G::kVecs);   // past the end: nothing is read
+        load(next, b + kGroup);   // past the end: nothing is read
         const float vmax = g.max();
         const bool guarded = !(__fmul_rn(g.min(), c) > -kSafe);
-        bool look = guarded || !(vmax <= m);
-        if constexpr (kTop) look |= !(vmax <= top.floor);
-        if (__any_sync(kAll, look)) {
-            if (__any_sync(kAll, !(vmax <= m))) raise(vmax);
-            if constexpr (kTop) {
-                if (__any_sync(kAll, !(vmax <= top.floor))) {
-                    bool at_least = false;
-                    if (first_group && top.floor != top.floor) {
-                        // k of the lanes' largest are at least the k-th of them
-                        const uint64_t k = sort_descending(rank_key(vmax, 0), lane);
-                        at_least = true;
-                        top.floor = key_value(__shfl_sync(kAll, k, a.top - 1));
-                    }
-                    int count = 0;
-#pragma unroll
-                    for (int u = 0; u < G::kVecs; ++u) {
-                        const int v = b + u * kThreads + tid;
-                        const float um = g.vec_max(u);
-                        if (!__any_sync(kAll, at_least ? !(um < top.floor) : !(um <= top.floor))) continue;
-                        float x[kN];
-                        V::unpack(g.raw[u], x);
-#pragma unroll
-                        for (int i = 0; i < kN; ++i)
-                            top_gather(top, s_found[warp], count, x[i], v < end, at_least,
-                                       static_cast<uint32_t>(sp.head + v * kN + i), lane, a.top);
-                    }
-                    top_flush(top, s_found[warp], count, lane, a.top);
-                }
-                first_group = false;
+        if constexpr (kTop) {
+            seg_max = max_nan(seg_max, vmax);
+            if (++in_seg == seg_groups) {
+                s_seg[seg++][tid] = seg_max;
+                lane_max = max_nan(lane_max, seg_max);
+                seg_max = ninf;
+                in_seg = 0;
             }
         }
+        bool careful = false;
+        if (__any_sync(kAll, guarded || !(vmax <= m))) {
+            if (__any_sync(kAll, !(vmax <= m))) raise(vmax);
+            careful = __any_sync(kAll, guarded);
+        }
         const float mc = __fmul_rn(m, c);
-        if (__any_sync(kAll, guarded) || !(fabsf(mc) < kSafe)) {
+        if (careful || !(fabsf(mc) < kSafe)) {
 #pragma unroll
             for (int u = 0; u < G::kVecs; ++u) {
                 float x[kN];
@@ -364,9 +367,85 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) k_logprobs(const __gri
             }
         }
     }
-    if (part == parts - 1) {
-        const int64_t done = sp.head + sp.vecs * kN;
-        if (done < a.vocab) scalars(done, static_cast<int>(a.vocab - done));
+    if (tail > 0) scalars(done, tail);
+
+    if constexpr (kTop) {
+        if (in_seg > 0) {
+            s_seg[seg++][tid] = seg_max;
+            lane_max = max_nan(lane_max, seg_max);
+        }
+        if (tid == 0) s_segs_found = s_found_total = 0;
+        s_top[warp][lane] = sort_descending(rank_key(lane_max, tid), lane);
+        __syncthreads();
+        merge_warps(s_top, warp, lane);
+        const float bound = key_value(s_top[0][a.top - 1]);
+        for (int q = 0; q < seg; ++q) {
+            if (s_seg[q][tid] < bound) continue;
+            const uint32_t at = atomicAdd(&s_segs_found, 1u);
+            if (at < kMaxFound) s_list[at] = static_cast<uint32_t>(q) * kThreads + tid;
+        }
+        __syncthreads();
+        const uint32_t listed = s_segs_found;
+        bool full = listed > kMaxFound;
+        if (!full) {
+            // candidates in no order: their keys decide
+            auto offer = [&](float x, bool ok, int64_t index) {
+                const bool want = ok && !(x < bound);
+                const unsigned who = __ballot_sync(kAll, want);
+                if (who == 0) return;
+                uint32_t at = 0;
+                if (lane == 0) at = atomicAdd(&s_found_total, static_cast<uint32_t>(__popc(who)));
+                at = __shfl_sync(kAll, at, 0) + __popc(who & ((1u << lane) - 1u));
+                if (want && at < kMaxFound) s_found[at] = rank_key(x, static_cast<uint32_t>(index));
+            };
+            for (uint32_t e = warp; e < listed; e += kWarps) {
+                const int q = static_cast<int>(s_list[e] / kThreads), t = static_cast<int>(s_list[e] % kThreads);
+                for (int g = q * seg_groups; g < groups && g < (q + 1) * seg_groups; ++g) {
+                    const int v = begin + g * kGroup + lane / kN % G::kVecs * kThreads + t;
+                    const int64_t index = sp.head + static_cast<int64_t>(v) * kN + lane % kN;
+                    const bool ok = v < end && lane < G::kVecs * kN && SPL_CHECK(index < a.vocab, kSiteTop, index);
+                    offer(ok ? V::load1(base, index) : ninf, ok, index);
+                }
+            }
+            if (warp == 0) {
+                offer(lane < head ? V::load1(base, lane) : ninf, lane < head, lane);
+                offer(lane < tail ? V::load1(base, done + lane) : ninf, lane < tail, done + lane);
+            }
+            __syncthreads();
+            full = s_found_total > kMaxFound;
+        }
+        TopList top = {0, nan_f()};
+        if (!full) {
+            if (warp == 0) top_flush(top, s_found, static_cast<int>(s_found_total), lane, a.top);
+        } else {   // the whole row again, each warp a list of its own
+            __syncthreads();
+            uint64_t* found = s_found + warp * 64;
+            int count = 0;
+            bool at_least = false;
+            if (warp == 0 && head > 0)
+                top_gather(top, found, count, lane < head ? V::load1(base, lane) : ninf, lane < head, at_least,
+                           static_cast<uint32_t>(lane), lane, a.top);
+            for (int b = begin; b < end; b += kThreads) {
+                const int v = b + tid;
+                at_least = true;   // equal values of a vector come in no order of their indices
+                float x[kN];
+                const uint32_t fill = kBf16 ? 0xff80ff80u : 0xff800000u;
+                V::unpack(v < end ? __ldcg(vecs + v) : make_uint4(fill, fill, fill, fill), x);
+                if (!__any_sync(kAll, v < end && !(vector_max(x) <= top.floor))) continue;
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+                    top_gather(top, found, count, x[i], v < end, at_least,
+                               static_cast<uint32_t>(sp.head + v * kN + i), lane, a.top);
+                top_flush(top, found, count, lane, a.top);
+                count = 0;
+            }
+            if (warp == 0 && tail > 0)
+                top_gather(top, found, count, lane < tail ? V::load1(base, done + lane) : ninf, lane < tail, at_least,
+                           static_cast<uint32_t>(done + lane), lane, a.top);
+            top_flush(top, found, count, lane, a.top);
+        }
+        __syncthreads();   // every thread has read the bound
+        s_top[warp][lane] = top.key;
     }
 
     // join: lanes (one reference), the CTA's warps
@@ -377,14 +456,8 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) k_logprobs(const __gri
         st.w = __fadd_rn(st.w, __shfl_xor_sync(kAll, st.w, off));
     }
     if (lane == 0) s_stats[warp] = st;
-    if constexpr (kTop) s_top[warp][lane] = top.key;
     __syncthreads();
-    if constexpr (kTop) {
-        for (int half = kWarps / 2; half > 0; half >>= 1) {
-            if (warp < half) s_top[warp][lane] = top_merge(s_top[warp][lane], s_top[warp + half][lane], lane);
-            __syncthreads();
-        }
-    }
+    if constexpr (kTop) merge_warps(s_top, warp, lane);
     const Stats none = {kLowest, 0.0f, 0.0f};
     if (warp == 0) st = join_warp(lane < kWarps ? s_stats[lane] : none, c);
     if (parts > 1) {   // the cluster's CTAs, in the first one
@@ -402,11 +475,7 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) k_logprobs(const __gri
                 __syncthreads();
                 s_top[warp][lane] = k;
                 __syncthreads();
-                for (int half = kWarps / 2; half > 0; half >>= 1) {
-                    if (warp < half)
-                        s_top[warp][lane] = top_merge(s_top[warp][lane], s_top[warp + half][lane], lane);
-                    __syncthreads();
-                }
+                merge_warps(s_top, warp, lane);
             }
         }
         cluster.sync();   // the other CTAs' shared memory has been read
@@ -555,6 +624,11 @@ cudaError_t launch_forward(const LogprobsArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     int parts = 1;
     while (parts < kMaxParts && a.rows * parts < 4 * sms && a.vocab / (2 * parts) >= 2048) parts *= 2;
+    if (parts > 8) {   // beyond the portable cluster size
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&k_logprobs<kBf16, kTop>),
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows * parts));
     cfg.blockDim = dim3(kThreads);
