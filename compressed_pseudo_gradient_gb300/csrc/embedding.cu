@@ -4,13 +4,15 @@
 //   out[t]     = scale table[id_t]
 //   d_table[v] = scale (sum of d_out[t] over the tokens t with id_t = v, in ascending t)
 //
-// The gradient first sorts the tokens by id (stable radix sort: digit counts per tile, a scan,
-// a ranked scatter), then sums over windows of kWindow consecutive sorted tokens: a run of
+// The gradient first sorts the tokens by id (up to kSmallSort of them in one CTA's shared memory,
+// more by a stable radix sort: digit counts per tile, a scan, a ranked scatter), then sums over
+// windows of consecutive sorted tokens: a run of
 // equal ids inside one window is summed and written at once, a run that crosses window borders
 // leaves one partial sum per window, joined in window order afterwards.  The work per CTA is
 // thus the same however often an id repeats, no floating-point atomics are used, and every run
-// gives the same bits.  Rows without tokens are zeroed by CTAs of the same launch, found in a
-// bitmap of the ids seen.
+// gives the same bits.  Rows without tokens are zeroed by CTAs of the summing launch, found in a
+// bitmap of the ids seen; beside a small sort, which leaves the GPU idle, the whole table is
+// zeroed instead.
 #include "local_device.cuh"
 #include "local_kernels.h"
 
@@ -220,8 +222,76 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const __grid_cons
     }
 }
 
+// ---- small sorts ----------------------------------------------------------------------------
+// Bitonic sort of (key, position) pairs in one CTA: positions are distinct, so the order is that
+// of the stable sort above.  The other CTAs of the launch zero the table meanwhile.
+constexpr int kSmallSort = 4096;
+constexpr int kSmallThreads = 1024;
+
+struct ZeroTable {
+    float* base;
+    int64_t rows, width, stride;   // rows = 0: nothing to zero
+};
+
+__global__ void __launch_bounds__(kSmallThreads)
+k_sort_small(const __grid_constant__ SortPass p, const __grid_constant__ ZeroTable z, int padded) {
+    const int tid = threadIdx.x;
+    if (blockIdx.x > 0) {
+        const int64_t ctas = gridDim.x - 1, cta = blockIdx.x - 1;
+        if (z.stride == z.width) {   // one range of memory: 16-byte stores between its ends
+            const int64_t n = z.rows * z.width;
+            const RowSplit sp = split_row<false>(z.base, n);
+            float4* v = reinterpret_cast<float4*>(z.base + sp.head);
+            for (int64_t i = cta * kSmallThreads + tid; i < sp.vecs; i += ctas * kSmallThreads)
+                if (SPL_CHECK(sp.head + 4 * (i + 1) <= n, kSiteRowsOut, i)) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int64_t done = sp.head + 4 * sp.vecs;
+            if (cta == 0 && tid < sp.head) z.base[tid] = 0.0f;
+            if (cta == 0 && tid < n - done) z.base[done + tid] = 0.0f;
+        } else {
+            for (int64_t r = cta; r < z.rows; r += ctas)
+                for (int64_t i = tid; i < z.width; i += kSmallThreads) z.base[r * z.stride + i] = 0.0f;
+        }
+        return;
+    }
+    __shared__ uint64_t s[kSmallSort];
+    for (int i = tid; i < padded; i += kSmallThreads) {
+        uint64_t e = ~0ull;
+        if (i < static_cast<int>(p.n)) {
+            const uint32_t key = sort_key(p, i);
+            if (key == p.vocab && p.flags != nullptr && token_at(p.ids, i) != p.padding_id)
+                atomicOr(p.flags, kFlagBadToken);
+            e = (static_cast<uint64_t>(key) << 32) | static_cast<uint32_t>(i);
+        }
+        s[i] = e;
+    }
+    __syncthreads();
+    for (int size = 2; size <= padded; size <<= 1) {
+        for (int off = size >> 1; off > 0; off >>= 1) {
+            for (int q = tid; q < padded / 2; q += kSmallThreads) {
+                const int i = (q / off) * 2 * off + q % off, j = i + off;   // off is a power of two
+                const uint64_t a = s[i], b = s[j];
+                if ((a > b) == ((i & size) == 0)) {
+                    s[i] = b;
+                    s[j] = a;
+                }
+            }
+            __syncthreads();
+        }
+    }
+    for (int i = tid; i < static_cast<int>(p.n); i += kSmallThreads) {
+        p.keys_out[i] = static_cast<uint32_t>(s[i] >> 32);
+        p.pos_out[i] = static_cast<uint32_t>(s[i]);
+    }
+}
+
 // ---- sums -----------------------------------------------------------------------------------
+// Sorted tokens per window.  Short windows give few tokens enough CTAs (2,000 tokens of width
+// 1001: SMALLWIN us with 16, 6 us with 64); long ones leave fewer partial sums.
 constexpr int kWindow = 64;
+constexpr int kShortWindow = 16;
+constexpr int kShortWindowTokens = 16384;   // up to this many tokens
+
+int window_of(int64_t count) { return count <= kShortWindowTokens ? kShortWindow : kWindow; }
 
 struct GradSums {
     const uint32_t* keys;   // sorted ids
@@ -232,7 +302,7 @@ struct GradSums {
     float* d_table;
     int64_t stride, width;
     float* partials;        // [window][head, tail][width]
-    uint32_t n, vocab, windows;
+    uint32_t n, vocab, windows, window;
     float scale;
     bool accumulate;
 };
@@ -298,14 +368,17 @@ __global__ void __launch_bounds__(kThreads)
 k_grad_windows(const __grid_constant__ GradSums g, int col_blocks, uint32_t window_ctas,
                uint32_t zero_rows) {
     using U = Unit<kBf16, kVec>;
-    if (blockIdx.x >= window_ctas) {   // zero the rows without tokens
-        const uint32_t row0 = (blockIdx.x - window_ctas) * zero_rows;
+    // the zeroing CTAs are spread between the summing ones, so that reads and writes mix
+    const uint64_t total = gridDim.x;
+    const uint32_t summing = static_cast<uint32_t>(blockIdx.x * static_cast<uint64_t>(window_ctas) / total);
+    if (static_cast<uint32_t>((blockIdx.x + 1ull) * window_ctas / total) == summing) {
+        const uint32_t row0 = (blockIdx.x - summing) * zero_rows;
         for (uint32_t r = row0; r < row0 + zero_rows && r < g.vocab; ++r) {
             if ((g.seen[r >> 5] >> (r & 31)) & 1u) continue;
             float* dst = g.d_table + r * g.stride;
             if constexpr (kVec) {
                 for (int64_t i = threadIdx.x; i < g.width / 4; i += blockDim.x)
-                    __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(0.f, 0.f, 0.f, 0.f));
+                    reinterpret_cast<float4*>(dst)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             } else {
                 for (int64_t i = threadIdx.x; i < g.width; i += blockDim.x) dst[i] = 0.0f;
             }
@@ -313,10 +386,10 @@ k_grad_windows(const __grid_constant__ GradSums g, int col_blocks, uint32_t wind
         return;
     }
     __shared__ uint32_t s_key[kWindow + 2], s_pos[kWindow];
-    const uint32_t win = blockIdx.x / col_blocks;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x % col_blocks) * blockDim.x + threadIdx.x;
-    const uint32_t first = win * kWindow;
-    const int count = min(static_cast<uint32_t>(kWindow), g.n - first);
+    const uint32_t win = summing / col_blocks;
+    const int64_t unit = static_cast<int64_t>(summing % col_blocks) * blockDim.x + threadIdx.x;
+    const uint32_t first = win * g.window;
+    const int count = min(g.window, g.n - first);
     for (int i = threadIdx.x; i < count + 2; i += blockDim.x) {
         const int64_t at = static_cast<int64_t>(first) + i - 1;
         s_key[i] = at < 0 || at >= g.n ? 0xffffffffu : g.keys[at];   // one past each end
@@ -364,7 +437,7 @@ k_grad_join(const __grid_constant__ GradSums g, int col_blocks) {
     using U = Unit<kBf16, kVec>;
     const uint32_t win = blockIdx.x / col_blocks;
     const int64_t unit = static_cast<int64_t>(blockIdx.x % col_blocks) * blockDim.x + threadIdx.x;
-    const uint32_t first = win * kWindow, next = first + kWindow;
+    const uint32_t first = win * g.window, next = first + g.window;
     const uint32_t key = g.keys[next - 1];
     if (key >= g.vocab || g.keys[next] != key) return;           // no run leaves this window
     if (first > 0 && g.keys[first] == key && g.keys[first - 1] == key) return;   // not its first
@@ -372,7 +445,7 @@ k_grad_join(const __grid_constant__ GradSums g, int col_blocks) {
     const int64_t col = unit * U::kN;
     U sum;
     sum.load_f32(g.partials + (2 * static_cast<int64_t>(win) + 1) * g.width + col);
-    for (uint32_t w = win + 1; w < g.windows && g.keys[w * kWindow] == key; ++w) {
+    for (uint32_t w = win + 1; w < g.windows && g.keys[w * g.window] == key; ++w) {
         U v;
         v.load_f32(g.partials + 2 * static_cast<int64_t>(w) * g.width + col);
         sum.add(v);
@@ -392,7 +465,7 @@ struct GradLayout {
 GradLayout grad_layout(int64_t count, int64_t vocab, int64_t width) {
     GradLayout l;
     l.tiles = static_cast<uint32_t>((count + kTile - 1) / kTile);
-    l.windows = static_cast<uint32_t>((count + kWindow - 1) / kWindow);
+    l.windows = static_cast<uint32_t>((count + window_of(count) - 1) / window_of(count));
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -420,7 +493,7 @@ cudaError_t launch_sums(const GradSums& g, cudaStream_t stream) {
     // rows zeroed per CTA: about 128 KB of them
     uint32_t zero_rows = static_cast<uint32_t>(32768 / g.width);
     if (zero_rows < 1) zero_rows = 1;
-    const uint32_t zero_ctas = g.accumulate ? 0 : (g.vocab + zero_rows - 1) / zero_rows;
+    const uint32_t zero_ctas = g.seen == nullptr ? 0 : (g.vocab + zero_rows - 1) / zero_rows;
     if (window_ctas + zero_ctas > 0) {
         k_grad_windows<kBf16, kVec><<<window_ctas + zero_ctas, threads, 0, stream>>>(
             g, static_cast<int>(col_blocks), window_ctas, zero_rows);
@@ -470,42 +543,56 @@ cudaError_t launch_embedding_grad(const EmbeddingGradArgs& a, bool bf16, cudaStr
     const GradLayout l = grad_layout(a.count, a.vocab, a.width);
     unsigned char* ws = static_cast<unsigned char*>(a.workspace);
     auto words = [&](size_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
-    cudaError_t e = cudaMemsetAsync(ws + l.seen, 0, (static_cast<size_t>(a.vocab) + 31) / 32 * 4, stream);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    const bool small = a.count <= kSmallSort;
+    const bool zero = !a.accumulate;
     int bits = 1;
     while ((a.vocab >> bits) != 0) ++bits;   // keys 0 .. vocab
-    const int passes = (bits + 9) / 10;
+    const int passes = small ? 1 : (bits + 9) / 10;
     const int digit = (bits + passes - 1) / passes;
     int in = 1;
-    if (a.count > 0) {
-        for (int pass = 0; pass < passes; ++pass) {
-            SortPass p = {};
-            p.ids = a.ids;
-            p.first = pass == 0;
-            p.keys_in = words(l.keys[in]);
-            p.pos_in = words(l.pos[in]);
-            p.keys_out = words(l.keys[in ^ 1]);
-            p.pos_out = words(l.pos[in ^ 1]);
-            p.counts = words(l.counts);
-            p.seen = words(l.seen);
-            p.flags = a.flags;
-            p.padding_id = a.padding_id;
-            p.n = static_cast<uint32_t>(a.count);
-            p.vocab = static_cast<uint32_t>(a.vocab);
-            p.tiles = l.tiles;
-            p.shift = pass * digit;
-            p.bits = digit;
+    if (!small && (e = cudaMemsetAsync(ws + l.seen, 0, (static_cast<size_t>(a.vocab) + 31) / 32 * 4, stream)) != cudaSuccess)
+        return e;
+    for (int pass = 0; pass < passes; ++pass) {
+        SortPass p = {};
+        p.ids = a.ids;
+        p.first = pass == 0;
+        p.keys_in = words(l.keys[in]);
+        p.pos_in = words(l.pos[in]);
+        p.keys_out = words(l.keys[in ^ 1]);
+        p.pos_out = words(l.pos[in ^ 1]);
+        p.counts = words(l.counts);
+        p.seen = words(l.seen);
+        p.flags = a.flags;
+        p.padding_id = a.padding_id;
+        p.n = static_cast<uint32_t>(a.count);
+        p.vocab = static_cast<uint32_t>(a.vocab);
+        p.tiles = l.tiles;
+        p.shift = pass * digit;
+        p.bits = digit;
+        if (small) {
+            int padded = 2, sms = 0, dev = 0;
+            while (padded < a.count) padded *= 2;
+            if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
+                (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+                return e;
+            // about 64 KB of the table per zeroing CTA, at most two per SM
+            const int64_t want = (a.vocab * a.width + 16383) / 16384, most = 2 * static_cast<int64_t>(sms) - 1;
+            const ZeroTable z = {a.d_table, zero ? a.vocab : 0, a.width, a.stride};
+            const unsigned ctas = zero ? static_cast<unsigned>(want < most ? want : most) : 0;
+            k_sort_small<<<1 + ctas, kSmallThreads, 0, stream>>>(p, z, padded);
+        } else {
             k_sort_count<<<l.tiles, kSortThreads, 0, stream>>>(p);
             k_sort_scan<<<1, 1024, 0, stream>>>(p.counts, l.tiles << digit);
             k_sort_scatter<<<l.tiles, kSortThreads, 0, stream>>>(p);
-            if ((e = cudaGetLastError()) != cudaSuccess) return e;
-            in ^= 1;
         }
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        in ^= 1;
     }
     GradSums g = {};
     g.keys = words(l.keys[in]);
     g.pos = words(l.pos[in]);
-    g.seen = words(l.seen);
+    g.seen = zero && !small ? words(l.seen) : nullptr;   // rows to zero, by their absence
     g.d_out = a.d_out;
     g.d_out_stride = a.d_out_stride;
     g.d_table = a.d_table;
@@ -515,6 +602,7 @@ cudaError_t launch_embedding_grad(const EmbeddingGradArgs& a, bool bf16, cudaStr
     g.n = static_cast<uint32_t>(a.count);
     g.vocab = static_cast<uint32_t>(a.vocab);
     g.windows = l.windows;
+    g.window = static_cast<uint32_t>(window_of(a.count));
     g.scale = a.scale;
     g.accumulate = a.accumulate;
     const bool vec = on16(a.d_out, a.d_out_stride, bf16 ? 2 : 4) && on16(a.d_table, a.stride, 4) &&

@@ -169,7 +169,7 @@ spl_status spl_embedding(const void* ids, int id_bits, size_t count, const void*
 
 static bool grad_sizes(size_t count, size_t vocab, size_t width) {
     return vocab >= 1 && vocab < kMaxDim && width >= 1 && width <= (size_t{1} << 30) &&
-           count <= kMaxDim && (count / 64 + 1) * (width / 256 + 1) + vocab <= kMaxGrid;
+           count <= kMaxDim && (count / 16 + 1) * (width / 256 + 1) + vocab <= kMaxGrid;
 }
 
 size_t spl_embedding_grad_workspace(size_t count, size_t vocab, size_t width) {

@@ -527,20 +527,39 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const __grid_constant_
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;
 
+// In the log2 domain t = log2 p = x c - lse log2 e, c = scale log2 e, with both factors as sums of
+// two fp32 numbers (the products' roundings would otherwise be as large as 2^-24 |lse|, in every
+// p alike), and dx = p (a + b t): a = -scale (g + h H), b = -scale h log 2.
 struct GradRow {
     float scale, lse, g, h, entropy;
+    float c_hi, c_lo, l_hi, l_lo;   // c, and lse log2 e
+    float a, b;
     int64_t target;   // -1: none
-    bool empty;
+    bool empty, fast;
 };
+
+constexpr float kLog2eRest = 1.92596299e-8f;   // log2 e less its fp32 value
+
+// v log2 e as a sum of two fp32 numbers.
+__device__ __forceinline__ void to_log2(float v, float& hi, float& lo) {
+    hi = __fmul_rn(v, kLog2e);
+    lo = __fmaf_rn(v, kLog2eRest, __fmaf_rn(v, kLog2e, -hi));
+}
 
 template <bool kEntropy>
 __device__ __forceinline__ float grad_value(float x, const GradRow& r) {
+    if (r.empty) return 0.0f;
+    if (r.fast && __fmul_rn(x, r.c_hi) > -kSafe) {
+        const float t = __fadd_rn(__fmaf_rn(x, r.c_hi, -r.l_hi), __fmaf_rn(x, r.c_lo, -r.l_lo));
+        return __fmul_rn(ex2(t), kEntropy ? __fmaf_rn(t, r.b, r.a) : r.a);
+    }
+    // masked: p is 0 (and d may be -inf), or NaN
     const float d = __fsub_rn(__fmul_rn(x, r.scale), r.lse);
     const float p = ex2(__fmul_rn(d, kLog2e));
     float v = -__fmul_rn(p, r.g);
-    if constexpr (kEntropy)   // p = 0: nothing (d may be -inf)
-        if (p > 0.0f) v = __fsub_rn(v, __fmul_rn(__fmul_rn(r.h, p), __fadd_rn(d, r.entropy)));
-    return v;
+    if constexpr (kEntropy)
+        if (!(p == 0.0f)) v = __fsub_rn(v, __fmul_rn(__fmul_rn(r.h, p), __fadd_rn(d, r.entropy)));
+    return __fmul_rn(v, r.scale);
 }
 
 template <bool kBf16, bool kEntropy>
@@ -556,14 +575,12 @@ k_logprobs_grad(const __grid_constant__ LogprobsGradArgs a, int parts, bool vect
 
     const RowSplit sp = split_row<kBf16>(in, a.vocab);
     const uint4* src = reinterpret_cast<const uint4*>(in + sp.head * V::kBytes);
-    const int64_t b = static_cast<int64_t>(part) * kGradThreads * kGradVecs + tid;
+    const int vecs = static_cast<int>(sp.vecs), b = part * (kGradThreads * kGradVecs) + tid;
     uint4 raw[kGradVecs];
     if (vectors) {
 #pragma unroll
-        for (int u = 0; u < kGradVecs; ++u) {
-            const int64_t v = b + u * kGradThreads;
-            if (v < sp.vecs) raw[u] = __ldcs(src + v);
-        }
+        for (int u = 0; u < kGradVecs; ++u)
+            if (b + u * kGradThreads < vecs) raw[u] = __ldcs(src + b + u * kGradThreads);
     }
 
     GradRow r;
@@ -578,12 +595,16 @@ k_logprobs_grad(const __grid_constant__ LogprobsGradArgs a, int parts, bool vect
     r.h = kEntropy ? a.d_entropy[row] : 0.0f;
     r.entropy = kEntropy ? a.entropy[row] : 0.0f;
     r.empty = r.lse == __uint_as_float(0xff800000u);
+    if (r.target < 0) r.target = -1;
+    to_log2(r.scale, r.c_hi, r.c_lo);
+    to_log2(r.lse, r.l_hi, r.l_lo);
+    r.a = -__fmul_rn(r.scale, __fmaf_rn(r.h, r.entropy, r.g));
+    r.b = -__fmul_rn(__fmul_rn(r.scale, r.h), kLn2);
+    r.fast = fabsf(r.l_hi) < kSafe && r.c_hi < kSafe && !r.empty;
 
     auto value = [&](float x, int64_t j) {
-        if (r.empty) return 0.0f;
-        float v = grad_value<kEntropy>(x, r);
-        if (j == r.target) v = __fadd_rn(v, r.g);
-        return __fmul_rn(v, r.scale);
+        const float v = grad_value<kEntropy>(x, r);
+        return j == r.target && !r.empty ? __fadd_rn(v, __fmul_rn(r.g, r.scale)) : v;
     };
 
     if (!vectors) {
@@ -595,15 +616,41 @@ k_logprobs_grad(const __grid_constant__ LogprobsGradArgs a, int parts, bool vect
         return;
     }
     uint4* dst = reinterpret_cast<uint4*>(out + sp.head * V::kBytes);
+    // the vector and the place in it that hold the target
+    const int64_t from_head = r.target - sp.head;
+    const int target_vec = r.target >= sp.head && !r.empty ? static_cast<int>(from_head / kN) : -1;
+    const int target_at = static_cast<int>(from_head % kN);
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u) {
-        const int64_t v = b + u * kGradThreads;
-        if (v >= sp.vecs || !SPL_CHECK(sp.head + (v + 1) * kN <= a.vocab, kSiteLogitsOut, v)) continue;
+        const int v = b + u * kGradThreads;
+        if (v >= vecs || !SPL_CHECK(sp.head + (static_cast<int64_t>(v) + 1) * kN <= a.vocab, kSiteLogitsOut, v))
+            continue;
         float x[kN];
         V::unpack(raw[u], x);
-        const int64_t first = sp.head + v * kN;
+        float low = x[0];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] = value(x[i], first + i);
+        for (int i = 1; i < kN; ++i) low = fminf(low, x[i]);
+        if (r.fast && __fmul_rn(low, r.c_hi) > -kSafe) {
+            const float2 ch = {r.c_hi, r.c_hi}, cl = {r.c_lo, r.c_lo}, lh = {-r.l_hi, -r.l_hi},
+                         ll = {-r.l_lo, -r.l_lo};
+#pragma unroll
+            for (int i = 0; i < kN; i += 2) {
+                const float2 xx = {x[i], x[i + 1]};
+                const float2 t = add2(fma2(xx, ch, lh), fma2(xx, cl, ll));
+                float2 f = {r.a, r.a};
+                if constexpr (kEntropy) f = fma2(t, make_float2(r.b, r.b), f);
+                x[i] = __fmul_rn(ex2(t.x), f.x);
+                x[i + 1] = __fmul_rn(ex2(t.y), f.y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) x[i] = grad_value<kEntropy>(x[i], r);
+        }
+        if (v == target_vec) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if (i == target_at) x[i] = __fadd_rn(x[i], __fmul_rn(r.g, r.scale));
+        }
         __stcs(dst + v, V::pack(x));
     }
     if (part == 0) {   // the ends around the whole vectors
