@@ -79,75 +79,181 @@ k_embedding(const __grid_constant__ EmbeddingArgs a, uint32_t units) {
 }
 
 // ---- sort by id -----------------------------------------------------------------------------
-// Least-significant-digit radix sort of (id, position) with digits of up to 10 bits.  A tile is
-// kTile consecutive entries, a warp's share of it consecutive too, so ranks by (tile, warp,
-// round, lane) keep equal digits in order.  Ids that take no part (padding, out of range) get
-// the key `vocab`, which sorts last.
-constexpr int kSortThreads = 256;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortRounds = 8;
-constexpr int kTile = kSortThreads * kSortRounds;
-constexpr int kMaxDigits = 1024;
-
-struct SortPass {
-    TokenIds ids;               // first pass: the call's ids
-    const uint32_t* keys_in;    // later passes
-    const uint32_t* pos_in;
-    uint32_t* keys_out;
-    uint32_t* pos_out;
-    uint32_t* counts;           // [digit][tile]
-    uint32_t* seen;             // bitmap of the ids that take part (first pass)
+// (id, position) pairs in order of (id, position).  Ids that take no part (padding, out of range)
+// get the key `vocab`, which sorts last.
+struct SortArgs {
+    TokenIds ids;
+    uint32_t* keys[2];   // the sorted pairs end up in keys[passes & 1], pos[passes & 1]
+    uint32_t* pos[2];
+    uint32_t* counts;    // [tile][digit]
+    uint32_t* seen;      // bitmap of the ids that take part, zero at launch
+    uint32_t* arrived;   // grid barrier counters, zero at launch
     uint32_t* flags;
     int64_t padding_id;
-    uint32_t n, vocab, tiles;
-    int shift, bits;
-    bool first;
+    uint32_t n, vocab;
+    uint32_t tiles, tile;   // CTAs that sort, and the tokens of each
+    int passes;
 };
 
-__device__ __forceinline__ uint32_t sort_key(const SortPass& p, uint32_t i) {
-    if (!p.first) return p.keys_in[i];
+__device__ __forceinline__ uint32_t id_key(const SortArgs& p, uint32_t i) {
     const int64_t id = token_at(p.ids, i);
     return id < 0 || id >= p.vocab || id == p.padding_id ? p.vocab : static_cast<uint32_t>(id);
 }
 
-__global__ void __launch_bounds__(kSortThreads) k_sort_count(const __grid_constant__ SortPass p) {
-    __shared__ uint32_t s_count[kMaxDigits];
-    const int digits = 1 << p.bits;
-    for (int d = threadIdx.x; d < digits; d += kSortThreads) s_count[d] = 0;
-    __syncthreads();
-    for (int r = 0; r < kSortRounds; ++r) {
-        const uint32_t i = blockIdx.x * kTile + r * kSortThreads + threadIdx.x;
-        if (i >= p.n || !SPL_CHECK(i < p.n, kSiteSorted, i)) continue;
-        const uint32_t key = sort_key(p, i);
-        atomicAdd(&s_count[(key >> p.shift) & (digits - 1)], 1u);
-        if (p.first) {
-            if (key < p.vocab) {
-                atomicOr(&p.seen[key >> 5], 1u << (key & 31));
-            } else if (p.flags != nullptr) {
-                const int64_t id = token_at(p.ids, i);
-                if (id != p.padding_id) atomicOr(p.flags, kFlagBadToken);
-            }
-        }
-    }
-    __syncthreads();
-    for (int d = threadIdx.x; d < digits; d += kSortThreads)
-        p.counts[static_cast<size_t>(d) * p.tiles + blockIdx.x] = s_count[d];
+__device__ __forceinline__ void flag_bad_id(const SortArgs& p, uint32_t i, uint32_t key) {
+    if (key == p.vocab && p.flags != nullptr && token_at(p.ids, i) != p.padding_id)
+        atomicOr(p.flags, kFlagBadToken);
 }
 
-// Exclusive prefix sums of n counts, in place, by one CTA.
-__global__ void __launch_bounds__(1024) k_sort_scan(uint32_t* __restrict__ counts, uint32_t n) {
-    __shared__ uint32_t s_warp[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t carry = 0;
-    for (uint32_t base = 0; base < n; base += 4096) {
-        const uint32_t i = base + threadIdx.x * 4;
-        uint32_t v[4], sum = 0;
+// The table, for CTAs that zero it while others sort (rows = 0: nothing to zero).
+struct ZeroTable {
+    float* base;
+    int64_t rows, width, stride;
+};
+
+__device__ __forceinline__ void zero_table(const ZeroTable& z, int64_t cta, int64_t ctas) {
+    const int tid = threadIdx.x, threads = blockDim.x;
+    if (z.stride == z.width) {   // one range of memory: 16-byte stores between its ends
+        const int64_t n = z.rows * z.width;
+        const RowSplit sp = split_row<false>(z.base, n);
+        float4* v = reinterpret_cast<float4*>(z.base + sp.head);
+        for (int64_t i = cta * threads + tid; i < sp.vecs; i += ctas * threads)
+            if (SPL_CHECK(sp.head + 4 * (i + 1) <= n, kSiteRowsOut, i)) __stcs(v + i, make_float4(0.f, 0.f, 0.f, 0.f));
+        const int64_t done = sp.head + 4 * sp.vecs;
+        if (cta == 0 && tid < sp.head) z.base[tid] = 0.0f;
+        if (cta == 0 && tid < n - done) z.base[done + tid] = 0.0f;
+    } else {
+        for (int64_t r = cta; r < z.rows; r += ctas)
+            for (int64_t i = tid; i < z.width; i += threads) z.base[r * z.stride + i] = 0.0f;
+    }
+}
+
+// Few tokens: a token's place is the number of tokens that sort before it, counted against all
+// keys in shared memory by kRankLanes threads.  No step waits for another CTA: SMALLSORT us.
+constexpr int kRankTokens = 8192;    // most tokens sorted this way
+constexpr int kRankThreads = 256;
+constexpr int kRankLanes = 8;
+
+__global__ void __launch_bounds__(kRankThreads)
+k_sort_rank(const __grid_constant__ SortArgs p, const __grid_constant__ ZeroTable z) {
+    constexpr uint32_t kPerCta = kRankThreads / kRankLanes;
+    if (blockIdx.x >= p.tiles) {
+        zero_table(z, blockIdx.x - p.tiles, gridDim.x - p.tiles);
+        return;
+    }
+    __shared__ uint32_t s_key[kRankTokens];
+    const uint32_t lanes = threadIdx.x % kRankLanes, i = blockIdx.x * kPerCta + threadIdx.x / kRankLanes;
+    for (uint32_t j = threadIdx.x; j < p.n; j += kRankThreads) {
+        const uint32_t key = id_key(p, j);
+        s_key[j] = key;
+        if (blockIdx.x == 0) flag_bad_id(p, j, key);
+    }
+    __syncthreads();
+    const uint32_t key = i < p.n ? s_key[i] : 0;
+    uint32_t before = 0;
+#pragma unroll 8
+    for (uint32_t j = lanes; j < p.n; j += kRankLanes)
+        before += s_key[j] < key || (s_key[j] == key && j < i);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = sum;
-            sum += i + k < n ? counts[i + k] : 0u;
+    for (int off = kRankLanes / 2; off > 0; off >>= 1) before += __shfl_xor_sync(kAll, before, off);
+    if (lanes == 0 && i < p.n && SPL_CHECK(before < p.n, kSiteSorted, before)) {
+        p.keys[1][before] = key;
+        p.pos[1][before] = i;
+    }
+}
+
+// More tokens: least-significant-digit radix sort with digits of kDigitBits in one cooperative
+// kernel.  A CTA has one tile of consecutive entries, a warp a consecutive share of it, so ranks
+// by (tile, warp, round, lane) keep equal digits in order.  Per pass: every warp counts its
+// digits, the tiles' counts go to memory, and after a barrier over the sorting CTAs each adds up
+// for itself what lies before its own entries.  65,536 tokens: SORTBIG us.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigitBits = 10;
+constexpr int kDigits = 1 << kDigitBits;   // one per thread
+constexpr int kSortSmem = kSortWarps * kDigits * 4;
+constexpr int kMaxSortBarriers = 8;
+
+// Waits (bounded) until all sorting CTAs have arrived; false on a timeout.
+__device__ __forceinline__ bool sort_barrier(const SortArgs& p, int step) {
+    __threadfence();
+    __syncthreads();
+    bool ok = true;
+    if (threadIdx.x == 0) {
+        uint32_t* counter = p.arrived + step;
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
+        uint32_t v;
+        const uint64_t t0 = global_ns();
+        do {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+        } while (v < p.tiles && (ok = global_ns() - t0 <= kWaitLimitNs));
+    }
+    ok = __syncthreads_and(ok) != 0;
+    __threadfence();
+    return ok;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1)
+k_sort_radix(const __grid_constant__ SortArgs p, const __grid_constant__ ZeroTable z) {
+    if (blockIdx.x >= p.tiles) {
+        zero_table(z, blockIdx.x - p.tiles, gridDim.x - p.tiles);
+        return;
+    }
+    extern __shared__ uint32_t s_count[];   // [warp][digit]
+    __shared__ uint32_t s_warp[kSortWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t share = p.tile / kSortWarps;   // a multiple of 32
+    const uint32_t first = blockIdx.x * p.tile + warp * share;
+    uint32_t* mine = s_count + warp * kDigits;
+
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * kDigitBits;
+        const uint32_t* keys_in = p.keys[pass & 1];
+        const uint32_t* pos_in = p.pos[pass & 1];
+        uint32_t* keys_out = p.keys[(pass & 1) ^ 1];
+        uint32_t* pos_out = p.pos[(pass & 1) ^ 1];
+        auto key_at = [&](uint32_t i) { return pass == 0 ? id_key(p, i) : __ldcg(keys_in + i); };
+
+        for (int d = lane; d < kDigits; d += 32) mine[d] = 0;
+        __syncwarp();
+        for (uint32_t r = 0; r < share; r += 32) {
+            const uint32_t i = first + r + lane;
+            const bool ok = i < p.n && SPL_CHECK(i < p.n, kSiteSorted, i);
+            const uint32_t key = ok ? key_at(i) : 0u;
+            // entries past the end share a value no digit has and are not counted
+            const uint32_t d = ok ? (key >> shift) & (kDigits - 1) : 0xffffffffu;
+            const unsigned peers = __match_any_sync(kAll, d);
+            if (ok && lane == __ffs(peers) - 1) mine[d] += __popc(peers);
+            if (pass == 0 && ok) {
+                if (key < p.vocab) {
+                    if (p.seen != nullptr) atomicOr(&p.seen[key >> 5], 1u << (key & 31));
+                } else {
+                    flag_bad_id(p, i, key);
+                }
+            }
+            __syncwarp();
         }
-        uint32_t scan = sum;
+        __syncthreads();
+        uint32_t total = 0;   // thread = digit: where each warp's entries start within the tile's
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) {
+            const uint32_t c = s_count[w * kDigits + tid];
+            s_count[w * kDigits + tid] = total;
+            total += c;
+        }
+        p.counts[static_cast<size_t>(blockIdx.x) * kDigits + tid] = total;
+        if (!sort_barrier(p, 2 * pass)) {
+            if (tid == 0 && p.flags != nullptr) atomicOr(p.flags, kFlagTimeout);
+            return;
+        }
+        uint32_t before = 0, all = 0;
+#pragma unroll 8
+        for (uint32_t t = 0; t < p.tiles; ++t) {
+            const uint32_t c = __ldcg(p.counts + static_cast<size_t>(t) * kDigits + tid);
+            if (t < blockIdx.x) before += c;
+            all += c;
+        }
+        uint32_t scan = all;   // over the digits
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const uint32_t o = __shfl_up_sync(kAll, scan, off);
@@ -165,122 +271,29 @@ __global__ void __launch_bounds__(1024) k_sort_scan(uint32_t* __restrict__ count
             s_warp[lane] = w;
         }
         __syncthreads();
-        const uint32_t before = carry + (warp > 0 ? s_warp[warp - 1] : 0u) + scan - sum;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i + k < n) counts[i + k] = before + v[k];
-        carry += s_warp[31];
+        const uint32_t start = (warp > 0 ? s_warp[warp - 1] : 0u) + scan - all + before;
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) s_count[w * kDigits + tid] += start;
         __syncthreads();
-    }
-}
-
-__global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const __grid_constant__ SortPass p) {
-    __shared__ uint32_t s_rank[kSortWarps][kMaxDigits];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int digits = 1 << p.bits;
-    for (int d = threadIdx.x; d < kSortWarps * kMaxDigits; d += kSortThreads) (&s_rank[0][0])[d] = 0;
-    __syncthreads();
-    uint32_t key[kSortRounds], rank[kSortRounds];
-    const uint32_t base = blockIdx.x * kTile + warp * (32 * kSortRounds) + lane;
-#pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) key[r] = base + r * 32 < p.n ? sort_key(p, base + r * 32) : 0u;
-#pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        const bool ok = base + r * 32 < p.n;
-        // entries past the end share a value no digit has and take no rank
-        const uint32_t d = ok ? (key[r] >> p.shift) & (digits - 1) : 0xffffffffu;
-        const unsigned peers = __match_any_sync(kAll, d);
-        const int lead = __ffs(peers) - 1;
-        uint32_t before = 0;
-        if (lane == lead && ok) {
-            before = s_rank[warp][d];
-            s_rank[warp][d] = before + __popc(peers);
+        for (uint32_t r = 0; r < share; r += 32) {
+            const uint32_t i = first + r + lane;
+            const bool ok = i < p.n;
+            const uint32_t key = ok ? key_at(i) : 0u;
+            const uint32_t d = ok ? (key >> shift) & (kDigits - 1) : 0xffffffffu;
+            const unsigned peers = __match_any_sync(kAll, d);
+            uint32_t to = ok ? mine[d] : 0u;
+            __syncwarp();
+            if (ok && lane == __ffs(peers) - 1) mine[d] = to + __popc(peers);
+            to += __popc(peers & ((1u << lane) - 1u));
+            __syncwarp();
+            if (!ok || !SPL_CHECK(to < p.n, kSiteSorted, to)) continue;
+            keys_out[to] = key;
+            pos_out[to] = pass == 0 ? i : __ldcg(pos_in + i);
         }
-        before = __shfl_sync(kAll, before, lead);
-        rank[r] = before + __popc(peers & ((1u << lane) - 1u));
-        __syncwarp();
-    }
-    __syncthreads();
-    for (int d = threadIdx.x; d < digits; d += kSortThreads) {   // start of each warp's share
-        uint32_t at = p.counts[static_cast<size_t>(d) * p.tiles + blockIdx.x];
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t c = s_rank[w][d];
-            s_rank[w][d] = at;
-            at += c;
+        if (pass + 1 < p.passes && !sort_barrier(p, 2 * pass + 1)) {
+            if (tid == 0 && p.flags != nullptr) atomicOr(p.flags, kFlagTimeout);
+            return;
         }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        const uint32_t i = base + r * 32;
-        if (i >= p.n) continue;
-        const uint32_t to = s_rank[warp][(key[r] >> p.shift) & (digits - 1)] + rank[r];
-        if (!SPL_CHECK(to < p.n, kSiteSorted, to)) continue;
-        p.keys_out[to] = key[r];
-        p.pos_out[to] = p.first ? i : p.pos_in[i];
-    }
-}
-
-// ---- small sorts ----------------------------------------------------------------------------
-// Bitonic sort of (key, position) pairs in one CTA: positions are distinct, so the order is that
-// of the stable sort above.  The other CTAs of the launch zero the table meanwhile.
-constexpr int kSmallSort = 4096;
-constexpr int kSmallThreads = 1024;
-
-struct ZeroTable {
-    float* base;
-    int64_t rows, width, stride;   // rows = 0: nothing to zero
-};
-
-__global__ void __launch_bounds__(kSmallThreads)
-k_sort_small(const __grid_constant__ SortPass p, const __grid_constant__ ZeroTable z, int padded) {
-    const int tid = threadIdx.x;
-    if (blockIdx.x > 0) {
-        const int64_t ctas = gridDim.x - 1, cta = blockIdx.x - 1;
-        if (z.stride == z.width) {   // one range of memory: 16-byte stores between its ends
-            const int64_t n = z.rows * z.width;
-            const RowSplit sp = split_row<false>(z.base, n);
-            float4* v = reinterpret_cast<float4*>(z.base + sp.head);
-            for (int64_t i = cta * kSmallThreads + tid; i < sp.vecs; i += ctas * kSmallThreads)
-                if (SPL_CHECK(sp.head + 4 * (i + 1) <= n, kSiteRowsOut, i)) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int64_t done = sp.head + 4 * sp.vecs;
-            if (cta == 0 && tid < sp.head) z.base[tid] = 0.0f;
-            if (cta == 0 && tid < n - done) z.base[done + tid] = 0.0f;
-        } else {
-            for (int64_t r = cta; r < z.rows; r += ctas)
-                for (int64_t i = tid; i < z.width; i += kSmallThreads) z.base[r * z.stride + i] = 0.0f;
-        }
-        return;
-    }
-    __shared__ uint64_t s[kSmallSort];
-    for (int i = tid; i < padded; i += kSmallThreads) {
-        uint64_t e = ~0ull;
-        if (i < static_cast<int>(p.n)) {
-            const uint32_t key = sort_key(p, i);
-            if (key == p.vocab && p.flags != nullptr && token_at(p.ids, i) != p.padding_id)
-                atomicOr(p.flags, kFlagBadToken);
-            e = (static_cast<uint64_t>(key) << 32) | static_cast<uint32_t>(i);
-        }
-        s[i] = e;
-    }
-    __syncthreads();
-    for (int size = 2; size <= padded; size <<= 1) {
-        for (int off = size >> 1; off > 0; off >>= 1) {
-            for (int q = tid; q < padded / 2; q += kSmallThreads) {
-                const int i = (q / off) * 2 * off + q % off, j = i + off;   // off is a power of two
-                const uint64_t a = s[i], b = s[j];
-                if ((a > b) == ((i & size) == 0)) {
-                    s[i] = b;
-                    s[j] = a;
-                }
-            }
-            __syncthreads();
-        }
-    }
-    for (int i = tid; i < static_cast<int>(p.n); i += kSmallThreads) {
-        p.keys_out[i] = static_cast<uint32_t>(s[i] >> 32);
-        p.pos_out[i] = static_cast<uint32_t>(s[i]);
     }
 }
 
@@ -303,6 +316,8 @@ struct GradSums {
     int64_t stride, width;
     float* partials;        // [window][head, tail][width]
     uint32_t n, vocab, windows, window;
+    // a CTA's threads: `cols` of them side by side on a window's units, the rest on more windows
+    uint32_t cols, col_blocks;
     float scale;
     bool accumulate;
 };
@@ -321,11 +336,26 @@ struct Unit {
 #pragma unroll
         for (int i = 0; i < kN; ++i) x[i] = __fadd_rn(x[i], o.x[i]);
     }
-    __device__ __forceinline__ void load_in(const void* row, int64_t unit) {
-        if constexpr (kVec)
-            Vec16<kBf16>::unpack(__ldcs(static_cast<const uint4*>(row) + unit), x);
-        else
-            x[0] = Vec16<kBf16>::load1(row, unit);
+    // One unit of the input as it lies in memory: loads in flight take no more registers.
+    struct Raw {
+        uint4 v;
+        float x;
+    };
+    static __device__ __forceinline__ Raw load_in(const void* row, int64_t unit) {
+        Raw r;
+        if constexpr (kVec) r.v = __ldcs(static_cast<const uint4*>(row) + unit);
+        else r.x = Vec16<kBf16>::load1(row, unit);
+        return r;
+    }
+    __device__ __forceinline__ void add(const Raw& r) {
+        if constexpr (kVec) {
+            float y[kN];
+            Vec16<kBf16>::unpack(r.v, y);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) x[i] = __fadd_rn(x[i], y[i]);
+        } else {
+            x[0] = __fadd_rn(x[0], r.x);
+        }
     }
     __device__ __forceinline__ void load_f32(const float* p) {
         if constexpr (kVec) {
@@ -364,88 +394,109 @@ struct Unit {
 // partial (it continues the previous window) or to its tail partial (it starts here and goes
 // on).
 template <bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kThreads)
-k_grad_windows(const __grid_constant__ GradSums g, int col_blocks, uint32_t window_ctas,
-               uint32_t zero_rows) {
+__global__ void __launch_bounds__(kThreads, 4)
+k_grad_windows(const __grid_constant__ GradSums g, uint32_t sum_ctas, uint32_t zero_rows) {
     using U = Unit<kBf16, kVec>;
-    // the zeroing CTAs are spread between the summing ones, so that reads and writes mix
-    const uint64_t total = gridDim.x;
-    const uint32_t summing = static_cast<uint32_t>(blockIdx.x * static_cast<uint64_t>(window_ctas) / total);
-    if (static_cast<uint32_t>((blockIdx.x + 1ull) * window_ctas / total) == summing) {
-        const uint32_t row0 = (blockIdx.x - summing) * zero_rows;
+    if (blockIdx.x >= sum_ctas) {   // zero the rows without tokens
+        const uint32_t row0 = (blockIdx.x - sum_ctas) * zero_rows;
         for (uint32_t r = row0; r < row0 + zero_rows && r < g.vocab; ++r) {
             if ((g.seen[r >> 5] >> (r & 31)) & 1u) continue;
             float* dst = g.d_table + r * g.stride;
             if constexpr (kVec) {
-                for (int64_t i = threadIdx.x; i < g.width / 4; i += blockDim.x)
-                    reinterpret_cast<float4*>(dst)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int64_t i = threadIdx.x; i < g.width / 4; i += kThreads)
+                    __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(0.f, 0.f, 0.f, 0.f));
             } else {
-                for (int64_t i = threadIdx.x; i < g.width; i += blockDim.x) dst[i] = 0.0f;
+                for (int64_t i = threadIdx.x; i < g.width; i += kThreads) dst[i] = 0.0f;
             }
         }
         return;
     }
-    __shared__ uint32_t s_key[kWindow + 2], s_pos[kWindow];
-    const uint32_t win = summing / col_blocks;
-    const int64_t unit = static_cast<int64_t>(summing % col_blocks) * blockDim.x + threadIdx.x;
-    const uint32_t first = win * g.window;
-    const int count = min(g.window, g.n - first);
-    for (int i = threadIdx.x; i < count + 2; i += blockDim.x) {
-        const int64_t at = static_cast<int64_t>(first) + i - 1;
-        s_key[i] = at < 0 || at >= g.n ? 0xffffffffu : g.keys[at];   // one past each end
-        if (i < count) s_pos[i] = g.pos[first + i];
+    // windows of this CTA (per_cta of them, kThreads / cols), with one key past each end
+    constexpr int kMaxStaged = kThreads / 8 * kWindow + 2;
+    __shared__ uint32_t s_key[kMaxStaged], s_pos[kMaxStaged];
+    const uint32_t per_cta = kThreads / g.cols;
+    const uint32_t win0 = blockIdx.x / g.col_blocks * per_cta;
+    const uint32_t base = win0 * g.window, staged = min(per_cta * g.window, g.n - base);
+    for (uint32_t i = threadIdx.x; i < staged + 2; i += kThreads) {
+        const int64_t at = static_cast<int64_t>(base) + i - 1;
+        s_key[i] = at < 0 || at >= g.n ? 0xffffffffu : g.keys[at];
+        if (i < staged) s_pos[i] = g.pos[base + i];
     }
     __syncthreads();
-    if (unit * U::kN >= g.width) return;
+    const uint32_t sub = threadIdx.x / g.cols, win = win0 + sub;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x % g.col_blocks) * g.cols + threadIdx.x % g.cols;
+    if (win >= g.windows || unit * U::kN >= g.width) return;
+    const int first = static_cast<int>(sub * g.window), count = min(static_cast<int>(g.window), static_cast<int>(staged) - first);
+    const uint32_t* key = s_key + first + 1;   // key[-1] and key[count] are the neighbours
+    const uint32_t* pos = s_pos + first;
     const int64_t col = unit * U::kN;
+    const unsigned char* in = static_cast<const unsigned char*>(g.d_out);
     constexpr int kAhead = 8;
     U sum;
     sum.zero();
     int start = 0;   // of the current run
     for (int i0 = 0; i0 < count; i0 += kAhead) {
-        U v[kAhead];
+        typename U::Raw v[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-            if (i0 + j < count && s_key[i0 + j + 1] < g.vocab)
-                v[j].load_in(static_cast<const unsigned char*>(g.d_out) +
-                                 static_cast<int64_t>(s_pos[i0 + j]) * g.d_out_stride *
-                                     Vec16<kBf16>::kBytes, unit);
+            if (i0 + j < count && key[i0 + j] < g.vocab)
+                v[j] = U::load_in(in + static_cast<int64_t>(pos[i0 + j]) * g.d_out_stride * Vec16<kBf16>::kBytes, unit);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int i = i0 + j;
-            if (i >= count || s_key[i + 1] >= g.vocab) break;
+            if (i >= count || key[i] >= g.vocab) break;
             sum.add(v[j]);
-            const uint32_t key = s_key[i + 1];
             const bool last = i + 1 == count;
-            if (!last && s_key[i + 2] == key) continue;
-            const bool from_left = start == 0 && s_key[0] == key;
-            const bool to_right = last && s_key[i + 2] == key;
+            if (!last && key[i + 1] == key[i]) continue;
+            const bool from_left = start == 0 && key[-1] == key[i];
+            const bool to_right = last && key[i + 1] == key[i];
             if (from_left || to_right)
                 sum.store_f32(g.partials + (2 * static_cast<int64_t>(win) + (from_left ? 0 : 1)) * g.width + col);
-            else if (SPL_CHECK(key < g.vocab, kSiteRowsOut, key))
-                sum.finish(g.d_table + key * g.stride + col, g.scale, g.accumulate);
+            else if (SPL_CHECK(key[i] < g.vocab, kSiteRowsOut, key[i]))
+                sum.finish(g.d_table + key[i] * g.stride + col, g.scale, g.accumulate);
             sum.zero();
             start = i + 1;
         }
     }
 }
 
-// Joins the partial sums of a run that crosses windows; the window it starts in owns it.
+// Joins the partial sums of a run that crosses windows; the window it starts in owns it.  The
+// threads first find together, 32 windows at a time, how far the run reaches.
 template <bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kThreads)
-k_grad_join(const __grid_constant__ GradSums g, int col_blocks) {
+__global__ void __launch_bounds__(kThreads) k_grad_join(const __grid_constant__ GradSums g) {
     using U = Unit<kBf16, kVec>;
-    const uint32_t win = blockIdx.x / col_blocks;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x % col_blocks) * blockDim.x + threadIdx.x;
-    const uint32_t first = win * g.window, next = first + g.window;
-    const uint32_t key = g.keys[next - 1];
-    if (key >= g.vocab || g.keys[next] != key) return;           // no run leaves this window
-    if (first > 0 && g.keys[first] == key && g.keys[first - 1] == key) return;   // not its first
-    if (unit * U::kN >= g.width) return;
+    const uint32_t per_cta = kThreads / g.cols;
+    const uint32_t win = blockIdx.x / g.col_blocks * per_cta + threadIdx.x / g.cols;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x % g.col_blocks) * g.cols + threadIdx.x % g.cols;
+    const uint32_t lane = threadIdx.x & 31;
+    bool owns = win + 1 < g.windows && unit * U::kN < g.width;
+    uint32_t key = 0;
+    if (owns) {
+        const uint32_t first = win * g.window, next = first + g.window;
+        key = g.keys[next - 1];
+        owns = key < g.vocab && g.keys[next] == key &&                      // a run leaves this window
+               !(first > 0 && g.keys[first] == key && g.keys[first - 1] == key);   // and starts in it
+    }
+    uint32_t reach = win + 1;   // one past the run's last window
+    if (g.cols >= 32) {   // a warp has one window
+        if (!__any_sync(kAll, owns)) return;
+        const uint32_t k = __reduce_max_sync(kAll, owns ? key : 0u);
+        for (uint32_t w = win + 1;; w += 32) {
+            const bool in = w + lane < g.windows && g.keys[(w + lane) * g.window] == k;
+            const unsigned run = __ballot_sync(kAll, in);
+            reach = w + (run == kAll ? 32 : __ffs(~run) - 1);
+            if (run != kAll) break;
+        }
+        if (!owns) return;
+    } else {
+        if (!owns) return;
+        while (reach < g.windows && g.keys[reach * g.window] == key) ++reach;
+    }
     const int64_t col = unit * U::kN;
     U sum;
     sum.load_f32(g.partials + (2 * static_cast<int64_t>(win) + 1) * g.width + col);
-    for (uint32_t w = win + 1; w < g.windows && g.keys[w * g.window] == key; ++w) {
+#pragma unroll 4
+    for (uint32_t w = win + 1; w < reach; ++w) {
         U v;
         v.load_f32(g.partials + 2 * static_cast<int64_t>(w) * g.width + col);
         sum.add(v);
@@ -458,13 +509,14 @@ constexpr size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15);
 
 // Where each array of the gradient's workspace starts, and its size.
 struct GradLayout {
-    size_t keys[2], pos[2], counts, seen, partials, bytes;
-    uint32_t tiles, windows;
+    size_t keys[2], pos[2], counts, seen, arrived, partials, bytes;
+    uint32_t windows;
 };
+
+constexpr int kMaxTiles = 256;   // sorting CTAs; at most one per SM
 
 GradLayout grad_layout(int64_t count, int64_t vocab, int64_t width) {
     GradLayout l;
-    l.tiles = static_cast<uint32_t>((count + kTile - 1) / kTile);
     l.windows = static_cast<uint32_t>((count + window_of(count) - 1) / window_of(count));
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -476,35 +528,70 @@ GradLayout grad_layout(int64_t count, int64_t vocab, int64_t width) {
         l.keys[i] = take(static_cast<size_t>(count) * 4);
         l.pos[i] = take(static_cast<size_t>(count) * 4);
     }
-    l.counts = take(static_cast<size_t>(l.tiles) * kMaxDigits * 4);
-    l.seen = take((static_cast<size_t>(vocab) + 31) / 32 * 4);
+    const bool radix = count > kRankTokens;
+    l.counts = take(radix ? static_cast<size_t>(kMaxTiles) * kDigits * 4 : 0);
+    l.seen = take(radix ? (static_cast<size_t>(vocab) + 31) / 32 * 4 : 0);   // cleared up to `partials`
+    l.arrived = take(radix ? kMaxSortBarriers * 4 : 0);
     l.partials = take(static_cast<size_t>(l.windows) * 2 * static_cast<size_t>(width) * 4);
-    l.bytes = at;
+    l.bytes = at + 256;   // never nothing: 0 stands for sizes that are not accepted
     return l;
 }
 
 template <bool kBf16, bool kVec>
-cudaError_t launch_sums(const GradSums& g, cudaStream_t stream) {
+cudaError_t launch_sums(GradSums g, cudaStream_t stream) {
     using U = Unit<kBf16, kVec>;
     const int64_t units = (g.width + U::kN - 1) / U::kN;
-    const int threads = static_cast<int>(units >= kThreads ? kThreads : (units + 31) / 32 * 32);
-    const int64_t col_blocks = (units + threads - 1) / threads;
-    const uint32_t window_ctas = static_cast<uint32_t>(g.windows * col_blocks);
+    g.cols = 8;
+    while (g.cols < kThreads && g.cols < units) g.cols *= 2;
+    g.col_blocks = static_cast<uint32_t>((units + g.cols - 1) / g.cols);
+    const uint32_t per_cta = kThreads / g.cols;
+    const uint32_t sum_ctas = (g.windows + per_cta - 1) / per_cta * g.col_blocks;
     // rows zeroed per CTA: about 128 KB of them
     uint32_t zero_rows = static_cast<uint32_t>(32768 / g.width);
     if (zero_rows < 1) zero_rows = 1;
     const uint32_t zero_ctas = g.seen == nullptr ? 0 : (g.vocab + zero_rows - 1) / zero_rows;
-    if (window_ctas + zero_ctas > 0) {
-        k_grad_windows<kBf16, kVec><<<window_ctas + zero_ctas, threads, 0, stream>>>(
-            g, static_cast<int>(col_blocks), window_ctas, zero_rows);
+    if (sum_ctas + zero_ctas > 0) {
+        k_grad_windows<kBf16, kVec><<<sum_ctas + zero_ctas, kThreads, 0, stream>>>(g, sum_ctas, zero_rows);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    if (g.windows > 1) {
-        k_grad_join<kBf16, kVec><<<static_cast<uint32_t>((g.windows - 1) * col_blocks), threads, 0, stream>>>(
-            g, static_cast<int>(col_blocks));
-    }
+    if (g.windows > 1) k_grad_join<kBf16, kVec><<<sum_ctas, kThreads, 0, stream>>>(g);
     return cudaGetLastError();
+}
+
+// Enqueues the sort, and beside it the zeroing of the table if z has rows.
+cudaError_t launch_sort(SortArgs p, const ZeroTable& z, int sms, cudaStream_t stream) {
+    // about 64 KB of the table per zeroing CTA at least
+    const int64_t want = (z.rows * z.width + 16383) / 16384;
+    if (p.n <= kRankTokens) {
+        constexpr uint32_t kPerCta = kRankThreads / kRankLanes;
+        p.tiles = (p.n + kPerCta - 1) / kPerCta;
+        const int64_t most = 8 * static_cast<int64_t>(sms);
+        const uint32_t zeroing = static_cast<uint32_t>(want < most ? want : most);
+        if (p.tiles + zeroing > 0) k_sort_rank<<<p.tiles + zeroing, kRankThreads, 0, stream>>>(p, z);
+        return cudaGetLastError();
+    }
+    const void* kern = reinterpret_cast<const void*>(&k_sort_radix);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+    if (e != cudaSuccess) return e;
+    // at least 1,024 tokens per tile; a quarter of the SMs at least stay with the zeroing
+    const uint32_t most = static_cast<uint32_t>(z.rows > 0 ? sms - sms / 4 : sms);
+    const uint32_t cap = most < kMaxTiles ? most : kMaxTiles;
+    uint32_t per = (p.n + cap - 1) / cap;
+    p.tile = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
+    p.tiles = (p.n + p.tile - 1) / p.tile;
+    const int64_t room = sms - static_cast<int64_t>(p.tiles);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles + (want < room ? want : room)));
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = kSortSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_sort_radix, p, z);
 }
 
 template <bool kBf16, bool kVec>
@@ -543,64 +630,48 @@ cudaError_t launch_embedding_grad(const EmbeddingGradArgs& a, bool bf16, cudaStr
     const GradLayout l = grad_layout(a.count, a.vocab, a.width);
     unsigned char* ws = static_cast<unsigned char*>(a.workspace);
     auto words = [&](size_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
-    cudaError_t e;
-    const bool small = a.count <= kSmallSort;
-    const bool zero = !a.accumulate;
-    int bits = 1;
-    while ((a.vocab >> bits) != 0) ++bits;   // keys 0 .. vocab
-    const int passes = small ? 1 : (bits + 9) / 10;
-    const int digit = (bits + passes - 1) / passes;
-    int in = 1;
-    if (!small && (e = cudaMemsetAsync(ws + l.seen, 0, (static_cast<size_t>(a.vocab) + 31) / 32 * 4, stream)) != cudaSuccess)
-        return e;
-    for (int pass = 0; pass < passes; ++pass) {
-        SortPass p = {};
-        p.ids = a.ids;
-        p.first = pass == 0;
-        p.keys_in = words(l.keys[in]);
-        p.pos_in = words(l.pos[in]);
-        p.keys_out = words(l.keys[in ^ 1]);
-        p.pos_out = words(l.pos[in ^ 1]);
-        p.counts = words(l.counts);
-        p.seen = words(l.seen);
-        p.flags = a.flags;
-        p.padding_id = a.padding_id;
-        p.n = static_cast<uint32_t>(a.count);
-        p.vocab = static_cast<uint32_t>(a.vocab);
-        p.tiles = l.tiles;
-        p.shift = pass * digit;
-        p.bits = digit;
-        if (small) {
-            int padded = 2, sms = 0, dev = 0;
-            while (padded < a.count) padded *= 2;
-            if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
-                (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-                return e;
-            // about 64 KB of the table per zeroing CTA, at most two per SM
-            const int64_t want = (a.vocab * a.width + 16383) / 16384, most = 2 * static_cast<int64_t>(sms) - 1;
-            const ZeroTable z = {a.d_table, zero ? a.vocab : 0, a.width, a.stride};
-            const unsigned ctas = zero ? static_cast<unsigned>(want < most ? want : most) : 0;
-            k_sort_small<<<1 + ctas, kSmallThreads, 0, stream>>>(p, z, padded);
-        } else {
-            k_sort_count<<<l.tiles, kSortThreads, 0, stream>>>(p);
-            k_sort_scan<<<1, 1024, 0, stream>>>(p.counts, l.tiles << digit);
-            k_sort_scatter<<<l.tiles, kSortThreads, 0, stream>>>(p);
-        }
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        in ^= 1;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const bool zero = !a.accumulate, radix = a.count > kRankTokens;
+    // Zeroing the whole table beside the sort writes the tokens' rows twice; with many tokens it
+    // is left to the summing kernel, which knows them from the bitmap.
+    const bool zero_all = zero && (!radix || a.count * a.width <= (int64_t{1} << 25));
+    SortArgs p = {};
+    p.ids = a.ids;
+    for (int i = 0; i < 2; ++i) {
+        p.keys[i] = words(l.keys[i]);
+        p.pos[i] = words(l.pos[i]);
     }
+    p.counts = words(l.counts);
+    p.seen = zero && !zero_all ? words(l.seen) : nullptr;
+    p.arrived = words(l.arrived);
+    p.flags = a.flags;
+    p.padding_id = a.padding_id;
+    p.n = static_cast<uint32_t>(a.count);
+    p.vocab = static_cast<uint32_t>(a.vocab);
+    p.passes = 1;
+    if (radix) {
+        while ((a.vocab >> (kDigitBits * p.passes)) != 0) ++p.passes;   // keys 0 .. vocab
+        const size_t from = p.seen != nullptr ? l.seen : l.arrived;
+        e = cudaMemsetAsync(ws + from, 0, l.partials - from, stream);
+        if (e != cudaSuccess) return e;
+    }
+    const ZeroTable z = {a.d_table, zero_all ? a.vocab : 0, a.width, a.stride};
+    if ((e = launch_sort(p, z, sms, stream)) != cudaSuccess) return e;
     GradSums g = {};
-    g.keys = words(l.keys[in]);
-    g.pos = words(l.pos[in]);
-    g.seen = zero && !small ? words(l.seen) : nullptr;   // rows to zero, by their absence
+    g.keys = p.keys[p.passes & 1];
+    g.pos = p.pos[p.passes & 1];
+    g.seen = p.seen;   // rows to zero, by their absence
     g.d_out = a.d_out;
     g.d_out_stride = a.d_out_stride;
     g.d_table = a.d_table;
     g.stride = a.stride;
     g.width = a.width;
     g.partials = reinterpret_cast<float*>(ws + l.partials);
-    g.n = static_cast<uint32_t>(a.count);
-    g.vocab = static_cast<uint32_t>(a.vocab);
+    g.n = p.n;
+    g.vocab = p.vocab;
     g.windows = l.windows;
     g.window = static_cast<uint32_t>(window_of(a.count));
     g.scale = a.scale;
