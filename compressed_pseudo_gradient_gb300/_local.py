@@ -102,17 +102,20 @@ def token_logprobs(logits, targets=None, *, scale: float = 1.0, top: int = 0,
     rows, vocab = logits.shape
     dev, top = logits.device, int(top)
     ids, bits = (None, 64) if targets is None else _ids(targets, "targets", rows, dev)
-    logp, lse, entropy = torch.empty((3, rows), dtype=torch.float32, device=dev).unbind(0)
-    base = lse.data_ptr() - 4 * rows
-    top_ids = top_logp = id_out = logp_out = None
+    lse = torch.empty(rows, dtype=torch.float32, device=dev)
+    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+    logp = lp_out = top_ids = top_logp = id_out = logp_out = None
+    if ids is not None:
+        logp = torch.empty(rows, dtype=torch.float32, device=dev)
+        lp_out = logp.data_ptr()
     if top > 0:
         top_ids = torch.empty((rows, top), dtype=torch.int64, device=dev)
         top_logp = torch.empty((rows, top), dtype=torch.float32, device=dev)
         id_out, logp_out = top_ids.data_ptr(), top_logp.data_ptr()
     _call(lib.spl_token_logprobs, dev, logits.data_ptr(), _dt(logits), rows, vocab, stride, ids,
-          bits, scale, top, None if ids is None else base, base + 4 * rows, base + 8 * rows, id_out,
-          logp_out, _flags_ptr(flags, dev))
-    return TokenLogprobs(None if ids is None else logp, lse, entropy, top_ids, top_logp)
+          bits, scale, top, lp_out, lse.data_ptr(), entropy.data_ptr(), id_out, logp_out,
+          None if flags is None else _flags_ptr(flags, dev))
+    return TokenLogprobs(logp, lse, entropy, top_ids, top_logp)
 
 
 def token_logprobs_grad(logits, targets, lse, d_logp, *, entropy=None, d_entropy=None,

@@ -23,6 +23,7 @@
 
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "local_device.cuh"
 #include "local_kernels.h"
@@ -38,6 +39,7 @@ constexpr float kLoScale = 2048.0f;      // of the state's low plane
 constexpr int kPrepThreads = 256;
 constexpr int kMaxPartials = 1216;  // sums of squares per matrix: eight CTAs per SM
 constexpr int kMaxPhases = 160;     // of the run kernel below
+constexpr int kMaxSlots = 32;       // of matrices with counters of their own
 
 struct PrepArgs {
     const void* update;
@@ -104,7 +106,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_orth_norm(const __grid_constan
     using U = PrepUnit<kBf16, kVec>;
     __shared__ double s_sum[kPrepThreads / 32];
     const int64_t b = blockIdx.y;
-    if (blockIdx.x == 0 && b == 0 && threadIdx.x < kMaxPhases) p.arrived[threadIdx.x] = 0;
+    if (blockIdx.x == 0 && b == 0)
+        for (int i = threadIdx.x; i < kMaxPhases * kMaxSlots; i += kPrepThreads) p.arrived[i] = 0;
     const uint32_t per_row = static_cast<uint32_t>(p.cols / U::kN);
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kPrepThreads * kPrepUnits);
     double total = 0.0;
@@ -292,16 +295,18 @@ cudaError_t launch_prep(PrepArgs p, int64_t batch, bool tall, int sms, cudaStrea
 
 // ---- the products ---------------------------------------------------------------------------
 // All products of a call run in one persistent cooperative kernel, as a list of phases.  A phase
-// names the earlier one that every CTA must have finished (a counter per phase in the workspace).  A phase computes D = A B^T (B's rows along K) or D = A B
+// names the earlier ones it needs: a unit of work waits until all their units of the same matrix are
+// in memory (counted per phase and slot of matrices in the workspace).  The matrices of a stack so
+// follow one another through the phases, and one's waits are filled by the others' products.  A phase computes D = A B^T (B's rows along K) or D = A B
 // (B's rows along N) tile by tile, and for each tile
 //
 //   value = f_acc * accumulator + f1 * source1 + f2 * source2
 //
 // written as one fp16 plane (a symmetric product also to its mirrored place), as the state's two
 // planes, or as bf16 (in place or transposed).  Per CTA: one thread issues the operands' TMA loads
-// into a ring of stages, one the MMAs, one the TMA loads of the sources' 128 x 64 slabs, four
-// warps turn accumulators into results in the slabs' shared memory, and one thread issues the TMA
-// stores that take them from there.  Two accumulators in tensor memory let a tile's MMAs run under the previous tile's
+// into a ring of stages, one the MMAs, one the TMA loads of the sources' 128 x 64 slabs, two
+// sets of four warps turn accumulators into results in the slabs' shared memory, a slab each, and
+// one thread issues the TMA stores that take them from there.  Two accumulators in tensor memory let a tile's MMAs run under the previous tile's
 // epilogue.
 //
 // kPair = 2: two CTAs form a 256 x 256 tile (cta_group::2: each loads its 128 rows of A and half
@@ -317,9 +322,10 @@ constexpr int kStages = 4;
 constexpr int kOperandBytes = kBlock * kTileK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kPlaneBytes = kBlock * kSlab * 2;
-constexpr int kSlabBytes = 3 * kPlaneBytes;  // two source planes, replaced by results; a mirror
-constexpr int kSlabs = 2;
-constexpr int kRunThreads = 256;
+constexpr int kSlabBytes = 2 * kPlaneBytes;  // the sources, replaced by results; or one of each and
+                                             // its mirror image
+constexpr int kSlabs = 3;                    // one per set of epilogue warps, and one being filled
+constexpr int kRunThreads = 384;
 constexpr int kRunSmem = kStages * kStageBytes + kSlabs * kSlabBytes + 1024;
 constexpr int kMaxMatrices = 10;   // X's planes twice, the output, five m x m matrices
 constexpr uint8_t kNone = 255;
@@ -332,7 +338,7 @@ struct Phase {
     bool b_along_n, sym;
     bool reduce;      // sum the previous phase's partial accumulators instead of a product
     uint8_t splits;   // parts of K (results are kPartial unless 1); of a reduce: partials per tile
-    int16_t after;    // the phase that must be complete before this one, or -1
+    int16_t after[2]; // the phases that must be complete before this one, or -1
     int16_t first;    // the group of CTAs that takes the first unit
     int n, k;         // columns of the result, length of the product
     float f_acc, f1, f2;
@@ -342,9 +348,9 @@ struct OrthRun {
     CUtensorMap wide[kMaxMatrices];     // boxes of 64 columns x 128 rows
     CUtensorMap narrow[kMaxMatrices];   // 64 x 64
     Phase phases[kMaxPhases];
-    int num_phases, m, batch;
+    int num_phases, m, batch, slots;
     float* partials;      // [unit][column / 4][row][4] of kPartial phases
-    uint32_t* arrived;    // a counter per phase, zero at launch
+    uint32_t* arrived;    // a counter per phase and slot, zero at launch
     uint32_t* flags;
 };
 
@@ -431,8 +437,8 @@ __device__ __forceinline__ void tmem_load_32(uint32_t addr, uint32_t* v) {
 
 __device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-// Waits until `count` CTAs have arrived on a phase's counter; bounded.
-__device__ __forceinline__ bool grid_wait(const uint32_t* counter, uint32_t count) {
+// Waits until a counter has reached `count`; bounded.
+__device__ __forceinline__ bool counter_wait(const uint32_t* counter, uint32_t count) {
     uint32_t v;
     uint64_t t0 = 0;
     for (;;) {
@@ -494,6 +500,33 @@ struct Tiling {
     }
 };
 
+// Matrices b with b % slots = s share the counters of slot s.
+__host__ __device__ __forceinline__ int matrices_of(int batch, int slots, int s) {
+    return batch / slots + (s < batch % slots ? 1 : 0);
+}
+
+// A role's waits for the phases before its units: each (phase, slot) once.
+template <int kPair>
+struct Dependencies {
+    int phase, slot;
+    __device__ __forceinline__ Dependencies() : phase(-1), slot(-1) {}
+    __device__ __forceinline__ bool wait(const OrthRun& run, const Phase& p, int ph, int b) {
+        const int s = b % run.slots;
+        if (ph == phase && s == slot) return true;
+        phase = ph;
+        slot = s;
+        bool ok = true;
+        for (int i = 0; i < 2; ++i) {
+            const int q = p.after[i];
+            if (q < 0) continue;
+            const uint32_t units = Tiling<kPair>::units(run.m, matrices_of(run.batch, run.slots, s), run.phases[q]);
+            ok = ok && counter_wait(run.arrived + q * run.slots + s, units * kPair);
+        }
+        fence_async_all();   // what other CTAs' copies wrote, before this one's read it
+        return ok;
+    }
+};
+
 // Byte offset of 16-byte chunk c of row r in a 128-byte-swizzled plane.
 __device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
@@ -538,46 +571,75 @@ __device__ __forceinline__ void store_transposed(unsigned char* plane, int row, 
     }
 }
 
-// A thread's row of a slab: accumulators v to results in the slab's planes.
-template <int kSources, ResultKind kResult, bool kMirror>
+// A thread's row of a slab: accumulators v to results in the slab's planes.  Sources are read
+// ahead of the stores that may alias them.  A mirror image takes the second source's plane, so
+// every warp must have read that first (`all_read`).
+template <int kSources, ResultKind kResult, bool kMirror, typename AllRead>
 __device__ __forceinline__ void finish_row(unsigned char* slab, int row, float (&v)[kSlab], float f_acc,
-                                           float f1, float f2) {
+                                           float f1, float f2, AllRead all_read) {
+    constexpr int kChunks = kSlab / 8;
+    constexpr bool kTranspose = kMirror || kResult == kBf16Transposed;
+    // with the second plane reused, all of it first; otherwise in halves, for the registers' sake
+    constexpr int kAhead = kSources == 2 && kTranspose ? kChunks : kChunks / 2;
 #pragma unroll
-    for (int c = 0; c < kSlab / 8; ++c) {
-        float* x = v + 8 * c;
-        uint4* p0 = reinterpret_cast<uint4*>(slab + swizzled(row, c));
-        uint4* p1 = reinterpret_cast<uint4*>(slab + kPlaneBytes + swizzled(row, c));
-        float y[8];
+    for (int c0 = 0; c0 < kChunks; c0 += kAhead) {
+        uint4 r1[kAhead], r2[kAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], f_acc);
-        if constexpr (kSources == 2) {
-            unpack_half8(*p1, y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fmaf_rn(f2, y[i], x[i]);
+        for (int c = 0; c < kAhead; ++c) {
+            if constexpr (kSources >= 1) r1[c] = *reinterpret_cast<const uint4*>(slab + swizzled(row, c0 + c));
+            if constexpr (kSources == 2)
+                r2[c] = *reinterpret_cast<const uint4*>(slab + kPlaneBytes + swizzled(row, c0 + c));
         }
-        if constexpr (kSources >= 1) {
-            unpack_half8(*p0, y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fmaf_rn(f1, y[i], x[i]);
-        }
-        uint4 w;
-        if constexpr (kResult == kBf16 || kResult == kBf16Transposed) {
-            const float z[8] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
-            w = Vec16<true>::pack(z);
-        } else {
-            w = pack_half8(x);
-        }
-        if constexpr (kResult != kBf16Transposed) *p0 = w;
-        if constexpr (kResult == kState) {
-            unpack_half8(w, y);
+        for (int c = 0; c < kAhead; ++c) {
+            float* x = v + 8 * (c0 + c);
+            float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(__fsub_rn(x[i], y[i]), kLoScale);
-            *p1 = pack_half8(y);
+            for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], f_acc);
+            if constexpr (kSources == 2) {
+                unpack_half8(r2[c], y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = __fmaf_rn(f2, y[i], x[i]);
+            }
+            if constexpr (kSources >= 1) {
+                unpack_half8(r1[c], y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = __fmaf_rn(f1, y[i], x[i]);
+            }
+            uint4 w;
+            if constexpr (kResult == kBf16 || kResult == kBf16Transposed) {
+                const float z[8] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+                w = Vec16<true>::pack(z);
+            } else {
+                w = pack_half8(x);
+            }
+            if constexpr (kSources == 2 && kTranspose) r1[c] = w;   // stored below
+            else if constexpr (kResult != kBf16Transposed)
+                *reinterpret_cast<uint4*>(slab + swizzled(row, c0 + c)) = w;
+            if constexpr (kResult == kState) {
+                unpack_half8(w, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(__fsub_rn(x[i], y[i]), kLoScale);
+                *reinterpret_cast<uint4*>(slab + kPlaneBytes + swizzled(row, c0 + c)) = pack_half8(y);
+            }
+            if constexpr (kTranspose && kSources < 2) store_transposed(slab + kPlaneBytes, row, c0 + c, w);
         }
-        if constexpr (kMirror || kResult == kBf16Transposed)
-            store_transposed(slab + 2 * kPlaneBytes, row, c, w);
+        if constexpr (kSources == 2 && kTranspose) {
+            all_read();
+#pragma unroll
+            for (int c = 0; c < kAhead; ++c) {
+                if constexpr (kResult != kBf16Transposed)
+                    *reinterpret_cast<uint4*>(slab + swizzled(row, c0 + c)) = r1[c];
+                store_transposed(slab + kPlaneBytes, row, c0 + c, r1[c]);
+            }
+        }
     }
 }
+
+template <int kCount>
+using Count = std::integral_constant<int, kCount>;
+template <ResultKind kResult>
+using Result = std::integral_constant<ResultKind, kResult>;
 
 template <int kPair>
 __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_constant__ OrthRun run) {
@@ -588,7 +650,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char* slabs = stages + kStages * kStageBytes;
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2],
-        src_full[kSlabs], src_empty[kSlabs], done[kSlabs], drain;
+        src_full[kSlabs], src_empty[kSlabs], done[kSlabs], read[2], drain;
     __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = kPair == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
@@ -601,7 +663,8 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&acc_full[s], 1);
-            mbar_init(&acc_empty[s], 4 * kPair);
+            mbar_init(&acc_empty[s], 8 * kPair);
+            mbar_init(&read[s], 4);
         }
         for (int s = 0; s < kSlabs; ++s) {
             mbar_init(&src_full[s], 1);
@@ -611,7 +674,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
         mbar_init(&drain, 1);
         fence_async_smem();
     }
-    if (warp == 5) {
+    if (warp == 9) {
         if constexpr (kPair == 2) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                          ::"r"(smem_addr(&s_tmem)), "n"(2 * kAccCols) : "memory");
@@ -632,21 +695,21 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
     const uint32_t tmem = s_tmem;
     bool late = false;
 
-    if (warp == 4) {
+    if (warp == 8) {
         if (lane == 0) {   // operands
+            Dependencies<kPair> deps;
             int stage = 0, used = 0;
             uint32_t phase = 0;
             for (int ph = 0; ph < run.num_phases && !late; ++ph) {
                 const Phase p = run.phases[ph];
                 if (p.reduce) continue;
-                if (p.after >= 0 && !grid_wait(run.arrived + p.after, gridDim.x)) {
-                    late = true;
-                    break;
-                }
-                fence_async_all();
                 const int units = T::units(run.m, run.batch, p);
-                for (int u = (group + groups - p.first) % groups; u < units && !late; u += groups) {
+                for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
                     const UnitAt at = T::at(run.m, p, u);
+                    if (!deps.wait(run, p, ph, at.b)) {
+                        late = true;
+                        break;
+                    }
                     for (int kb = at.k0; kb < at.k1; ++kb) {
                         if (!mbar_wait(&empty[stage], phase ^ 1u)) {
                             late = true;
@@ -685,7 +748,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
             }
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == 9) {
         if (lane == 0 && rank == 0) {   // products
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
@@ -699,7 +762,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                 const uint32_t lead = p.b_along_n ? kOperandBytes / 2 : 16;
                 const uint32_t b_step = p.b_along_n ? 128 : 2;   // 16 of K: 16 rows, or 32 bytes
                 const int units = T::units(run.m, run.batch, p);
-                for (int u = (group + groups - p.first) % groups; u < units && !late; u += groups) {
+                for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
                     const UnitAt at = T::at(run.m, p, u);
                     if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u)) {
                         late = true;
@@ -737,22 +800,22 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
             }
         }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == 10) {
         if (lane == 0) {   // sources
+            Dependencies<kPair> deps;
             int buf = 0, used = 0;
             uint32_t phase = 0;
             for (int ph = 0; ph < run.num_phases && !late; ++ph) {
                 const Phase p = run.phases[ph];
-                if (p.after >= 0 && !grid_wait(run.arrived + p.after, gridDim.x)) {
-                    late = true;
-                    break;
-                }
-                fence_async_all();
                 const int units = T::units(run.m, run.batch, p);
-                for (int u = (group + groups - p.first) % groups; u < units && !late; u += groups) {
+                for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
                     const UnitAt at = T::at(run.m, p, u);
                     const int row = at.i * T::kTile + rank * kBlock;
                     if (row >= run.m) continue;
+                    if (!deps.wait(run, p, ph, at.b)) {
+                        late = true;
+                        break;
+                    }
                     for (int s = at.slab0; s < at.slab1; ++s) {
                         const int col = at.j * T::kTile + s * kSlab;
                         if (col >= p.n) break;
@@ -786,14 +849,14 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
             }
         }
         __syncwarp();
-    } else if (warp == 7) {
+    } else if (warp == 11) {
         if (lane == 0) {   // stores
-            int buf = 0;
+            int buf = 0, leaving = -1;   // the buffer whose stores may still read it
             uint32_t phase = 0;
             for (int ph = 0; ph < run.num_phases && !late; ++ph) {
                 const Phase p = run.phases[ph];
                 const int units = T::units(run.m, run.batch, p);
-                for (int u = (group + groups - p.first) % groups; u < units && !late; u += groups) {
+                for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
                     const UnitAt at = T::at(run.m, p, u);
                     const int row0 = at.i * T::kTile + rank * kBlock;
                     for (int s = at.slab0; s < at.slab1 && row0 < run.m; ++s) {
@@ -810,46 +873,55 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                             if (p.result == kState)
                                 tma_store(&run.wide[p.dst_lo], slab + kPlaneBytes, col0, row0, at.b);
                             if (transposed || (p.sym && at.i != at.j)) {
-                                tma_store(&run.narrow[p.dst], slab + 2 * kPlaneBytes, row0, col0, at.b);
+                                tma_store(&run.narrow[p.dst], slab + kPlaneBytes, row0, col0, at.b);
                                 if (row0 + 64 < run.m)
-                                    tma_store(&run.narrow[p.dst], slab + 2 * kPlaneBytes + kSlab * 128,
+                                    tma_store(&run.narrow[p.dst], slab + kPlaneBytes + kSlab * 128,
                                               row0 + 64, col0, at.b);
                             }
-                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                         }
-                        mbar_arrive(&src_empty[buf]);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        // the slab before this one has left its buffer
+                        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        if (leaving >= 0) mbar_arrive(&src_empty[leaving]);
+                        leaving = buf;
                         if (++buf == kSlabs) {
                             buf = 0;
                             phase ^= 1u;
                         }
                     }
-                }
-                // this CTA's results of the phase are in memory
-                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-                if (!late) {
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    if (leaving >= 0) mbar_arrive(&src_empty[leaving]);
+                    leaving = -1;
+                    // this CTA's results of the unit are in memory
+                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                    if (late) break;
                     fence_async_all();
-                    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(run.arrived + ph) : "memory");
+                    asm volatile("red.release.gpu.global.add.u32 [%0], 1;"
+                                 ::"l"(run.arrived + ph * run.slots + at.b % run.slots) : "memory");
                 }
             }
             if (late && run.flags != nullptr) atomicOr(run.flags, kFlagTimeout);
         }
         __syncwarp();
     } else {   // results
-        const int row_in = warp * 32 + lane;
-        int acc = 0, buf = 0;
-        uint32_t acc_phase = 0, phase = 0;
+        Dependencies<kPair> deps;
+        // warps 0-3 take the even slabs in the order of the CTA's work, 4-7 the odd ones
+        const int set = warp >> 2, quarter = warp & 3, row_in = quarter * 32 + lane;
+        int acc = 0, slab_count = 0;
+        uint32_t acc_phase = 0, read_phase = 0;
         for (int ph = 0; ph < run.num_phases && !late; ++ph) {
             const Phase p = run.phases[ph];
-            if (p.reduce) {
-                const bool ok = grid_wait(run.arrived + p.after, gridDim.x);
-                late = __any_sync(kAll, !ok);
-            }
             const int units = T::units(run.m, run.batch, p);
-            for (int u = (group + groups - p.first) % groups; u < units && !late; u += groups) {
+            for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
                 const UnitAt at = T::at(run.m, p, u);
                 const int row0 = at.i * T::kTile + rank * kBlock;
-                if (!p.reduce) {
+                if (p.reduce) {
+                    const bool ok = deps.wait(run, p, ph, at.b);
+                    if (__any_sync(kAll, !ok)) {
+                        late = true;
+                        break;
+                    }
+                } else {
                     const bool ok = mbar_wait(&acc_full[acc], acc_phase);
                     if (__any_sync(kAll, !ok)) {
                         late = true;
@@ -860,9 +932,12 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                 for (int s = at.slab0; s < at.slab1 && row0 < run.m; ++s) {
                     const int col0 = at.j * T::kTile + s * kSlab;
                     if (col0 >= p.n) break;
+                    const int buf = slab_count % kSlabs;
+                    const uint32_t phase = slab_count / kSlabs & 1;
+                    if ((slab_count++ & 1) != set) continue;
                     float v[kSlab];
                     if (!p.reduce) {
-                        const uint32_t from = tmem + (static_cast<uint32_t>(warp * 32) << 16) +
+                        const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                               acc * kAccCols + s * kSlab;
                         tmem_load_32(from, reinterpret_cast<uint32_t*>(v));
                         tmem_load_32(from + 32, reinterpret_cast<uint32_t*>(v) + 32);
@@ -903,29 +978,34 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                             }
                         }
                         const bool mirror = p.sym && at.i != at.j;
-                        if (p.result == kState)
-                            finish_row<2, kState, false>(slab, row_in, v, p.f_acc, p.f1, p.f2);
-                        else if (p.result == kBf16)
-                            finish_row<2, kBf16, false>(slab, row_in, v, p.f_acc, p.f1, p.f2);
-                        else if (p.result == kBf16Transposed)
-                            finish_row<2, kBf16Transposed, false>(slab, row_in, v, p.f_acc, p.f1, p.f2);
-                        else if (p.src1 == kNone)
-                            mirror ? finish_row<0, kPlane, true>(slab, row_in, v, p.f_acc, 0.0f, 0.0f)
-                                   : finish_row<0, kPlane, false>(slab, row_in, v, p.f_acc, 0.0f, 0.0f);
-                        else if (p.src2 == kNone)
-                            mirror ? finish_row<1, kPlane, true>(slab, row_in, v, p.f_acc, p.f1, 0.0f)
-                                   : finish_row<1, kPlane, false>(slab, row_in, v, p.f_acc, p.f1, 0.0f);
-                        else
-                            mirror ? finish_row<2, kPlane, true>(slab, row_in, v, p.f_acc, p.f1, p.f2)
-                                   : finish_row<2, kPlane, false>(slab, row_in, v, p.f_acc, p.f1, p.f2);
+                        // the four warps of the set have read this slab's sources
+                        auto all_read = [&] {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&read[set]);
+                            late |= !mbar_wait(&read[set], read_phase);
+                            read_phase ^= 1u;
+                        };
+                        auto finish = [&](auto sources, auto result, auto mirrored) {
+                            finish_row<decltype(sources)::value, decltype(result)::value, decltype(mirrored)::value>(
+                                slab, row_in, v, p.f_acc, p.f1, p.f2, all_read);
+                        };
+                        using Yes = std::true_type;
+                        using No = std::false_type;
+                        const Count<0> none;
+                        const Count<1> one;
+                        const Count<2> two;
+                        const Result<kPlane> plane;
+                        if (p.result == kState) finish(two, Result<kState>(), No());
+                        else if (p.result == kBf16) finish(two, Result<kBf16>(), No());
+                        else if (p.result == kBf16Transposed) finish(two, Result<kBf16Transposed>(), No());
+                        else if (p.src1 == kNone) mirror ? finish(none, plane, Yes()) : finish(none, plane, No());
+                        else if (p.src2 == kNone) mirror ? finish(one, plane, Yes()) : finish(one, plane, No());
+                        else mirror ? finish(two, plane, Yes()) : finish(two, plane, No());
+                        late = __any_sync(kAll, late);
                         fence_async_smem();
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&done[buf]);
-                    if (++buf == kSlabs) {
-                        buf = 0;
-                        phase ^= 1u;
-                    }
                 }
                 if (late) break;
                 if (!p.reduce) {
@@ -947,7 +1027,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
-    if (warp == 5) {
+    if (warp == 9) {
         if constexpr (kPair == 2)
             asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(2 * kAccCols));
         else
@@ -1038,7 +1118,7 @@ OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
     const int squares = may_group(l.m, l.n) ? kSquares : 2;
     for (int i = 0; i < kSquares; ++i)
         l.square[i] = i < squares ? take(static_cast<size_t>(batch * l.m * l.ldm) * 2) : 0;
-    l.arrived = take(kMaxPhases * 4);
+    l.arrived = take(kMaxPhases * kMaxSlots * 4);
     // partial accumulators of a split product: enough units for a few per SM, where its tiles
     // alone are fewer than that
     const int64_t blocks = (l.n + kTileK - 1) / kTileK, tm = (l.m + kBlock - 1) / kBlock;
@@ -1127,10 +1207,14 @@ struct PhaseList {
     int16_t last() const { return static_cast<int16_t>(num - 1); }
     void add(Phase ph) {
         ph.splits = 1;
-        ph.after = last();
+        ph.after[0] = last();
+        ph.after[1] = -1;
         phases[num++] = ph;
     }
-    void after(int16_t phase) { phases[num - 1].after = phase; }
+    void after(int16_t first, int16_t second = -1) {
+        phases[num - 1].after[0] = first;
+        phases[num - 1].after[1] = second;
+    }
     // A symmetric m x m product.
     void square(uint8_t a, uint8_t b, uint8_t src1, uint8_t src2, uint8_t dst, int m, int k, float f_acc,
                 float f1, float f2) {
@@ -1154,24 +1238,31 @@ struct PhaseList {
 
 // Estimated microseconds of a list of products on `groups` CTAs (or pairs), and with `out` the
 // phases to run: a symmetric product with fewer tiles than groups and a long K is split along K
-// where that pays, followed by a phase that sums the parts.  Measured: a block of 64 along K 0.14
-// us for a 128 x 128 tile and 0.27 us for a pair's 256 x 256 one, an epilogue of 128 columns 1.2 us,
-// and 4 us from a phase's last result to the next one's first product.
+// where that pays, followed by a phase that sums the parts.  Measured: a block of 64 along K takes
+// 0.28 us for a 128 x 128 tile alone on its SM (its 32 KB arrive from L2 no faster) and 0.44 us
+// with all SMs at it (L2's own limit), 0.32 us for a pair's 256 x 256 one; an epilogue of 128
+// columns 1.2 us; and 4 us from a phase's last result to the next one's first product, which other
+// matrices' work fills.
 template <int kPair>
 double plan(const PhaseList& list, const OrthRun& run, int groups, size_t partial_bytes, OrthRun* out) {
     using T = Tiling<kPair>;
-    const double block = kPair == 2 ? 0.27 : 0.14, epilogue = 1.2 * kPair, between = 4.0;
+    const int slots = run.batch < kMaxSlots ? run.batch : kMaxSlots;
+    const double epilogue = 1.2 * kPair, between = 4.0 / slots;
     const size_t unit_bytes = static_cast<size_t>(T::kTile) * T::kTile * 4;
     double total = 0.0;
     int index[kMaxPhases], num = 0, taken = 0;   // where each listed phase ends up
-    bool split = false;
+    bool split = false, any_split = false;
     for (int i = 0; i < list.num; ++i) {
         Phase ph = list.phases[i];
         const int tiles = T::tiles(run.m, ph) * run.batch, blocks = (ph.k + kTileK - 1) / kTileK;
         auto time = [&](int splits) {
-            const int units = tiles * splits, waves = (units + groups - 1) / groups;
+            const int units = tiles * splits;
+            const double full = units < groups ? static_cast<double>(units) / groups : 1.0;
+            const double block = kPair == 2 ? 0.32 : 0.28 + 0.16 * full;
             const double one = block * ((blocks + splits - 1) / splits);
-            double t = waves * (one > epilogue ? one : epilogue) + epilogue + between;
+            // a stack's phases flow into one another: no waves
+            const double waves = slots > 1 ? static_cast<double>(units) / groups : (units + groups - 1) / groups;
+            double t = waves * (one > epilogue ? one : epilogue) + (slots > 1 ? 0.0 : epilogue) + between;
             if (splits > 1) {
                 const int slabs = tiles * T::kTileSlabs;
                 t += (slabs + groups - 1) / groups * (1.0 + 0.25 * splits) + between;
@@ -1186,11 +1277,14 @@ double plan(const PhaseList& list, const OrthRun& run, int groups, size_t partia
                     best = q;
         total += time(best);
         // the parts of two products beside each other would share the partials' memory
-        if (i > 0 && (best > 1 || split)) ph.after = static_cast<int16_t>(i - 1);
+        if (i > 0 && (best > 1 || split)) ph.after[0] = static_cast<int16_t>(i - 1), ph.after[1] = -1;
         split = best > 1;
-        const bool beside = ph.after >= 0 && ph.after != i - 1;
-        ph.after = static_cast<int16_t>(ph.after < 0 ? -1 : index[ph.after]);
-        ph.first = static_cast<int16_t>(beside ? taken % groups : 0);
+        any_split |= split;
+        const bool beside = ph.after[0] >= 0 && ph.after[0] != i - 1;
+        for (int q = 0; q < 2; ++q)
+            ph.after[q] = static_cast<int16_t>(ph.after[q] < 0 ? -1 : index[ph.after[q]]);
+        // work goes on where the phase before it left off, if the two overlap
+        ph.first = static_cast<int16_t>(beside || slots > 1 ? taken % groups : 0);
         Phase sum = ph;
         if (best > 1) {
             ph.splits = static_cast<uint8_t>(best);
@@ -1203,13 +1297,19 @@ double plan(const PhaseList& list, const OrthRun& run, int groups, size_t partia
         if (best > 1) {
             sum.reduce = true;
             sum.splits = static_cast<uint8_t>(best);
-            sum.after = static_cast<int16_t>(num - 1);
+            sum.after[0] = static_cast<int16_t>(num - 1);
+            sum.after[1] = -1;
             sum.first = 0;
+            taken = tiles * T::kTileSlabs;
             if (out != nullptr) out->phases[num] = sum;
             index[i] = num++;
         }
     }
-    if (out != nullptr) out->num_phases = num;
+    if (out != nullptr) {
+        out->num_phases = num;
+        // partials of one matrix may lie where another's lay in an earlier phase
+        out->slots = any_split ? 1 : slots;
+    }
     return total;
 }
 
@@ -1346,16 +1446,19 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& a, bool bf16, cudaStre
             list.square(A, A, A, kNone, B, m, m, a.coef[2] / kGramScale, a.coef[1], 0.0f);
             const int16_t poly = list.last();
             uint8_t next = B;
+            int16_t rest = poly;
             if (R != kNone) {           // (a I + B) (f I + R) - a f I = a R + f B + B R
                 next = take();
                 list.square(B, R, R, B, next, m, m, 1.0f / kGramScale, ca, f);
                 f *= ca;
+                rest = list.last();
             }
             if (more) {                 // A <- (a I + B) A (a I + B); beside the product above
                 const uint8_t T = take();
                 list.square(B, A, A, kNone, T, m, m, 1.0f / kGramScale, ca, 0.0f);
                 list.after(poly);
                 list.square(T, B, T, kNone, A, m, m, 1.0f / kGramScale, ca, 0.0f);
+                list.after(static_cast<int16_t>(list.last() - 1), rest);
                 give(T);
             }
             if (R != kNone) {
