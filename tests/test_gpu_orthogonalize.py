@@ -44,7 +44,10 @@ def limit(m, n):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("m,n", [(1, 1), (1, 7), (9, 1), (2, 2), (8, 8), (17, 33), (64, 64), (63, 65), (100, 257),
                                  (128, 128), (129, 127), (200, 1000), (1000, 136), (256, 256), (257, 511), (384, 640),
-                                 (513, 700), (1000, 999), (96, 5000), (700, 2100)])
+                                 (513, 700), (1000, 999), (96, 5000), (700, 2100),
+                                 # around the sizes that one cluster holds
+                                 (128, 4096), (100, 4001), (4096, 31), (128, 4097), (64, 1100), (700, 128), (129, 256),
+                                 (256, 130), (255, 255), (256, 257), (200, 136)])
 def test_matrix(m, n, dtype):
     u = torch.randn(m, n, generator=gen(m * n), device=DEV).to(dtype) * 1e-3
     got = spl.orthogonalize(u)
