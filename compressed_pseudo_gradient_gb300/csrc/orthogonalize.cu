@@ -1144,28 +1144,26 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
         }
     }
 
-    // the update with its momentum step, as fp32 [row][column] in shared memory
+    // the update with its momentum step, as fp32 [row][column] in shared memory: a warp per stored
+    // line, kLines of them at a time for the loads in flight
+    const int lines = s.tall ? cols : rows, length = s.tall ? rows : cols;   // as stored
+    const int64_t line0 = s.tall ? col0 : row0, at0 = s.tall ? row0 : col0;
+    constexpr int kWarps = kSmallThreads / 32, kLines = 4;
     float sum = 0.0f;
-    {
-        const int lines = s.tall ? cols : rows, length = s.tall ? rows : cols;   // as stored
-        const int64_t line0 = s.tall ? col0 : row0, at0 = s.tall ? row0 : col0;
-        const int per_line = length > 0 ? (length + U::kN - 1) / U::kN : 0, total = lines > 0 ? lines * per_line : 0;
-        constexpr int kBatch = kVec ? 4 : 8;
-        for (int first = tid; first < total; first += kSmallThreads * kBatch) {
-            U g[kBatch], mom[kBatch];
+    for (int l0 = warp; l0 < lines; l0 += kWarps * kLines) {
+        for (int at = lane * U::kN; at < length; at += 32 * U::kN) {
+            U g[kLines], mom[kLines];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int i = first + k * kSmallThreads;
-                if (i >= total || !SPL_CHECK(i < total, kSiteOrthIn, i)) continue;
-                const int64_t line = line0 + i / per_line, at = at0 + i % per_line * U::kN;
-                g[k].load(p, b, line, at / U::kN);
-                if (p.momentum != nullptr) mom[k].load_momentum(p.momentum + (b * p.rows + line) * p.cols + at);
+            for (int k = 0; k < kLines; ++k) {
+                const int64_t line = line0 + l0 + k * kWarps;
+                if (l0 + k * kWarps >= lines || !SPL_CHECK(line < p.rows, kSiteOrthIn, line)) continue;
+                g[k].load(p, b, line, (at0 + at) / U::kN);
+                if (p.momentum != nullptr) mom[k].load_momentum(p.momentum + (b * p.rows + line) * p.cols + at0 + at);
             }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int i = first + k * kSmallThreads;
-                if (i >= total) continue;
-                const int line = i / per_line, at = i % per_line * U::kN;
+            for (int k = 0; k < kLines; ++k) {
+                const int line = l0 + k * kWarps;
+                if (line >= lines) continue;
 #pragma unroll
                 for (int e = 0; e < U::kN; ++e) {
                     if (p.momentum != nullptr) mom[k].x[e] = __fmaf_rn(p.mu, mom[k].x[e], g[k].x[e]);
@@ -1393,15 +1391,21 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
         if (!last) publish();
     }
     __syncthreads();
-    {
-        const int lines = s.tall ? cols : rows, length = s.tall ? rows : cols;
-        const int64_t line0 = s.tall ? col0 : row0, at0 = s.tall ? row0 : col0;
-        const int total = lines > 0 && length > 0 ? lines * length : 0;
-        for (int i = tid; i < total; i += kSmallThreads) {
-            const int line = i / length, at = i % length;
-            if (!SPL_CHECK(line < lines, kSiteOrthOut, line)) continue;
-            Vec16<true>::store1(s.out, (b * p.rows + line0 + line) * p.cols + at0 + at,
-                                staging[s.tall ? at * kStagePitch + line : line * kStagePitch + at]);
+    const int across = s.tall ? kStagePitch : 1, down = s.tall ? 1 : kStagePitch;   // along and between lines
+    for (int line = warp; line < lines; line += kWarps) {
+        uint16_t* out = s.out + (b * p.rows + line0 + line) * p.cols + at0;
+        const float* from = staging + line * down;
+        if ((p.cols & 1) == 0) {   // pairs of values stay on 4 bytes
+            for (int at = 2 * lane; at < length; at += 64) {
+                if (!SPL_CHECK(at < length, kSiteOrthOut, at)) continue;
+                const float lo = from[at * across], hi = from[(at + 1) * across];
+                uint32_t w;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+                *reinterpret_cast<uint32_t*>(out + at) = w;
+            }
+        } else {
+            for (int at = lane; at < length; at += 32)
+                if (SPL_CHECK(at < length, kSiteOrthOut, at)) Vec16<true>::store1(out, at, from[at * across]);
         }
     }
     if (late && tid == 0 && s.flags != nullptr) atomicOr(s.flags, kFlagTimeout);
