@@ -343,6 +343,7 @@ struct Phase {
     int16_t after[2]; // the phases that must be complete before this one, or -1
     int16_t first;    // the group of CTAs that takes the first unit
     int n, k;         // columns of the result, length of the product
+    int tile_n;       // columns of a tile: kTile, or half of a pair's
     float f_acc, f1, f2;
 };
 
@@ -462,33 +463,42 @@ struct UnitAt {
 
 template <int kPair>
 struct Tiling {
-    static constexpr int kTile = kBlock * kPair;   // rows and columns of a tile
-    static constexpr int kTileSlabs = kTile / kSlab;
+    static constexpr int kTile = kBlock * kPair;   // rows of a tile, and its columns at most
 
+    // Tiles of a symmetric product are those that reach the diagonal of their last row: tile row i
+    // has kTile / tile_n (i + 1) of them, the last one no more than there are.
     static __host__ __device__ __forceinline__ int tiles(int m, const Phase& p) {
-        const int tm = (m + kTile - 1) / kTile, tn = (p.n + kTile - 1) / kTile;
-        return p.sym ? tm * (tm + 1) / 2 : tm * tn;
+        const int tm = (m + kTile - 1) / kTile, tn = (p.n + p.tile_n - 1) / p.tile_n, ratio = kTile / p.tile_n;
+        if (!p.sym) return tm * tn;
+        const int in_last = ratio * tm < tn ? ratio * tm : tn;
+        return ratio * (tm * (tm - 1) / 2) + in_last;
     }
+    static __host__ __device__ __forceinline__ int slabs(const Phase& p) { return p.tile_n / kSlab; }
     // A reduce phase deals out single slabs, a split product parts of K.
     static __host__ __device__ __forceinline__ int units(int m, int batch, const Phase& p) {
-        return tiles(m, p) * batch * (p.reduce ? kTileSlabs : p.splits);
+        return tiles(m, p) * batch * (p.reduce ? slabs(p) : p.splits);
+    }
+    // Whether a tile of a symmetric product holds its own mirror image (or its neighbour does).
+    static __device__ __forceinline__ bool on_diagonal(const Phase& p, int i, int j) {
+        return j * p.tile_n / kTile == i;
     }
     static __device__ __forceinline__ UnitAt at(int m, const Phase& p, int u) {
         UnitAt a;
-        const int per = p.reduce ? kTileSlabs : p.splits;
+        const int per = p.reduce ? slabs(p) : p.splits;
         a.tile = u / per;
         const int part = u - a.tile * per;
         const int tiles_b = tiles(m, p);
         a.b = a.tile / tiles_b;
         const int r = a.tile - a.b * tiles_b;
-        if (p.sym) {   // tile row i starts at i (i + 1) / 2
-            int i = static_cast<int>((sqrtf(1.0f + 8.0f * static_cast<float>(r)) - 1.0f) * 0.5f);
-            while (i * (i + 1) / 2 > r) --i;
-            while ((i + 1) * (i + 2) / 2 <= r) ++i;
+        if (p.sym) {   // tile row i starts at ratio i (i + 1) / 2
+            const int ratio = kTile / p.tile_n;
+            int i = static_cast<int>((sqrtf(1.0f + 8.0f * static_cast<float>(r) / ratio) - 1.0f) * 0.5f);
+            while (ratio * (i * (i + 1) / 2) > r) --i;
+            while (ratio * ((i + 1) * (i + 2) / 2) <= r) ++i;
             a.i = i;
-            a.j = r - i * (i + 1) / 2;
+            a.j = r - ratio * (i * (i + 1) / 2);
         } else {       // groups of 8 tile rows, so that the tiles in flight share both operands
-            const int tm = (m + kTile - 1) / kTile, tn = (p.n + kTile - 1) / kTile;
+            const int tm = (m + kTile - 1) / kTile, tn = (p.n + p.tile_n - 1) / p.tile_n;
             const int g = r / (8 * tn), h = min(8, tm - 8 * g), q = r - g * 8 * tn;
             a.i = 8 * g + q % h;
             a.j = q / h;
@@ -497,7 +507,7 @@ struct Tiling {
         a.k0 = p.reduce ? 0 : blocks * part / p.splits;
         a.k1 = p.reduce ? 0 : blocks * (part + 1) / p.splits;
         a.slab0 = p.reduce ? part : 0;
-        a.slab1 = p.reduce ? part + 1 : kTileSlabs;
+        a.slab1 = p.reduce ? part + 1 : slabs(p);
         return a;
     }
 };
@@ -720,14 +730,18 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                         unsigned char* a = stages + stage * kStageBytes;
                         unsigned char* b = a + kOperandBytes;
                         const uint32_t bar = kPair == 2 ? leader_addr(&full[stage]) : smem_addr(&full[stage]);
-                        if (rank == 0) mbar_expect_tx(&full[stage], kPair * kStageBytes);
-                        const int row = at.i * T::kTile + rank * kBlock, col = at.j * T::kTile + rank * kBlock;
+                        const int cols = p.tile_n / kPair;   // of B per CTA: 128 or 64
+                        if (rank == 0) mbar_expect_tx(&full[stage], kPair * (kOperandBytes + cols * kTileK * 2));
+                        const int row = at.i * T::kTile + rank * kBlock, col = at.j * p.tile_n + rank * cols;
                         tma_load<kPair>(a, &run.wide[p.a], kb * kTileK, row, at.b, bar);
                         if (p.b_along_n) {
                             tma_load<kPair>(b, &run.narrow[p.b], col, kb * kTileK, at.b, bar);
-                            tma_load<kPair>(b + kOperandBytes / 2, &run.narrow[p.b], col + 64, kb * kTileK, at.b, bar);
+                            if (cols > 64)
+                                tma_load<kPair>(b + kOperandBytes / 2, &run.narrow[p.b], col + 64, kb * kTileK, at.b,
+                                                bar);
                         } else {
-                            tma_load<kPair>(b, &run.wide[p.b], kb * kTileK, col, at.b, bar);
+                            tma_load<kPair>(b, cols > 64 ? &run.wide[p.b] : &run.narrow[p.b], kb * kTileK, col, at.b,
+                                            bar);
                         }
                         if (used < kStages) ++used;
                         if (++stage == kStages) {
@@ -759,7 +773,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                 if (p.reduce) continue;
                 // fp32 accumulators, fp16 operands, B transposed where its rows run along N
                 const uint32_t idesc = (1u << 4) | ((p.b_along_n ? 1u : 0u) << 16) |
-                                       (static_cast<uint32_t>(T::kTile / 8) << 17) |
+                                       (static_cast<uint32_t>(p.tile_n / 8) << 17) |
                                        (static_cast<uint32_t>(T::kTile / 16) << 24);
                 const uint32_t lead = p.b_along_n ? kOperandBytes / 2 : 16;
                 const uint32_t b_step = p.b_along_n ? 128 : 2;   // 16 of K: 16 rows, or 32 bytes
@@ -819,7 +833,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                         break;
                     }
                     for (int s = at.slab0; s < at.slab1; ++s) {
-                        const int col = at.j * T::kTile + s * kSlab;
+                        const int col = at.j * p.tile_n + s * kSlab;
                         if (col >= p.n) break;
                         if (!mbar_wait(&src_empty[buf], phase ^ 1u)) {
                             late = true;
@@ -862,7 +876,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                     const UnitAt at = T::at(run.m, p, u);
                     const int row0 = at.i * T::kTile + rank * kBlock;
                     for (int s = at.slab0; s < at.slab1 && row0 < run.m; ++s) {
-                        const int col0 = at.j * T::kTile + s * kSlab;
+                        const int col0 = at.j * p.tile_n + s * kSlab;
                         if (col0 >= p.n) break;
                         if (!mbar_wait(&done[buf], phase)) {
                             late = true;
@@ -874,7 +888,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                             if (!transposed) tma_store(&run.wide[p.dst], slab, col0, row0, at.b);
                             if (p.result == kState)
                                 tma_store(&run.wide[p.dst_lo], slab + kPlaneBytes, col0, row0, at.b);
-                            if (transposed || (p.sym && at.i != at.j)) {
+                            if (transposed || (p.sym && !T::on_diagonal(p, at.i, at.j))) {
                                 tma_store(&run.narrow[p.dst], slab + kPlaneBytes, row0, col0, at.b);
                                 if (row0 + 64 < run.m)
                                     tma_store(&run.narrow[p.dst], slab + kPlaneBytes + kSlab * 128,
@@ -894,10 +908,10 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     if (leaving >= 0) mbar_arrive(&src_empty[leaving]);
                     leaving = -1;
-                    // this CTA's results of the unit are in memory
+                    // once the stores are complete their results are visible to this thread, and
+                    // to others through its release
                     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
                     if (late) break;
-                    fence_async_all();
                     asm volatile("red.release.gpu.global.add.u32 [%0], 1;"
                                  ::"l"(run.arrived + ph * run.slots + at.b % run.slots) : "memory");
                 }
@@ -932,7 +946,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 }
                 for (int s = at.slab0; s < at.slab1 && row0 < run.m; ++s) {
-                    const int col0 = at.j * T::kTile + s * kSlab;
+                    const int col0 = at.j * p.tile_n + s * kSlab;
                     if (col0 >= p.n) break;
                     const int buf = slab_count % kSlabs;
                     const uint32_t phase = slab_count / kSlabs & 1;
@@ -979,7 +993,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                                 }
                             }
                         }
-                        const bool mirror = p.sym && at.i != at.j;
+                        const bool mirror = p.sym && !T::on_diagonal(p, at.i, at.j);
                         // the four warps of the set have read this slab's sources
                         auto all_read = [&] {
                             __syncwarp();
@@ -1596,7 +1610,7 @@ cudaError_t run_limits(RunLimits* out) {
     return cudaSuccess;
 }
 
-// How many of the first steps are taken as one polynomial of A, applied to X once.  Per step X
+// How many of the first steps may be taken as one polynomial of A, applied to X once.  Per step X
 // costs 3 m^2 n multiplications (the symmetric product counts half) and A m^3; a group of g costs
 // 3 m^2 n + (4 g - 3) m^3, less as soon as n > m.  The iteration's last steps undo the roundings
 // of its first ones, so only those are grouped, and at least two steps stay single: 64-bit
@@ -1650,45 +1664,60 @@ struct PhaseList {
 };
 
 // Estimated microseconds of a list of products on `groups` CTAs (or pairs), and with `out` the
-// phases to run: a symmetric product with fewer tiles than groups and a long K is split along K
-// where that pays, followed by a phase that sums the parts.  Measured: a block of 64 along K takes
-// 0.28 us for a 128 x 128 tile alone on its SM (its 32 KB arrive from L2 no faster) and 0.44 us
-// with all SMs at it (L2's own limit), 0.32 us for a pair's 256 x 256 one; an epilogue of 128
-// columns 1.2 us; and 4 us from a phase's last result to the next one's first product, which other
-// matrices' work fills.
+// phases to run.  A pair's tiles have 256 or 128 columns, whichever the model prefers; a symmetric
+// product with fewer tiles than groups and a long K is split along K where that pays, followed by
+// a phase that sums the parts.  Measured: a block of 64 along K takes 0.28 us for a 128 x 128 tile
+// alone on its SM (its 32 KB arrive from L2 no faster) and 0.44 us with all SMs at it (L2's own
+// limit), 0.32 us for a pair's 256 x 256 tile and 0.2 us for 256 x 128; an epilogue 1 us and 0.8 us
+// for each slab of 64 columns, two slabs at a time; and 5 us from a phase's last result to the
+// next one's first product.  A stack's phases flow into one another, so that they take either the
+// time of their work or one matrix's way through them.
 template <int kPair>
 double plan(const PhaseList& list, const OrthRun& run, int groups, size_t partial_bytes, OrthRun* out) {
     using T = Tiling<kPair>;
     const int slots = run.batch < kMaxSlots ? run.batch : kMaxSlots;
-    const double epilogue = 1.2 * kPair, between = 4.0 / slots;
+    constexpr double kBetween = 5.0;
     const size_t unit_bytes = static_cast<size_t>(T::kTile) * T::kTile * 4;
     double total = 0.0;
     int index[kMaxPhases], num = 0, taken = 0;   // where each listed phase ends up
     bool split = false, any_split = false;
     for (int i = 0; i < list.num; ++i) {
         Phase ph = list.phases[i];
-        const int tiles = T::tiles(run.m, ph) * run.batch, blocks = (ph.k + kTileK - 1) / kTileK;
-        auto time = [&](int splits) {
-            const int units = tiles * splits;
+        const int blocks = (ph.k + kTileK - 1) / kTileK;
+        auto time = [&](int tile_n, int splits) {
+            Phase q = ph;
+            q.tile_n = tile_n;
+            const int tiles = T::tiles(run.m, q) * run.batch, units = tiles * splits;
             const double full = units < groups ? static_cast<double>(units) / groups : 1.0;
-            const double block = kPair == 2 ? 0.32 : 0.28 + 0.16 * full;
-            const double one = block * ((blocks + splits - 1) / splits);
-            // a stack's phases flow into one another: no waves
-            const double waves = slots > 1 ? static_cast<double>(units) / groups : (units + groups - 1) / groups;
-            double t = waves * (one > epilogue ? one : epilogue) + (slots > 1 ? 0.0 : epilogue) + between;
-            if (splits > 1) {
-                const int slabs = tiles * T::kTileSlabs;
-                t += (slabs + groups - 1) / groups * (1.0 + 0.25 * splits) + between;
+            const double block = kPair == 1 ? 0.28 + 0.16 * full : tile_n == 256 ? 0.32 : 0.2;
+            const double one = block * ((blocks + splits - 1) / splits), epilogue = 0.4 * (tile_n / kSlab);
+            const double work = one > epilogue ? one : epilogue;
+            const double through = one + 1.0 + epilogue + kBetween;   // one unit, alone
+            double t = (units + groups - 1) / groups * work - work + through;
+            if (slots > 1) {
+                const double flow = static_cast<double>(units) / groups * work;
+                t = flow > through ? flow : through;
             }
+            if (splits > 1)
+                t += (tiles * T::slabs(q) + groups - 1) / groups * (1.0 + 0.25 * splits) + kBetween;
             return t;
         };
         int best = 1;
-        if (ph.sym)
-            for (int q = 2; q <= kMaxSplits && q <= blocks / kSplitBlocks; ++q)
-                if (static_cast<size_t>(tiles) * q * unit_bytes <= partial_bytes && num + 3 < kMaxPhases &&
-                    time(q) < time(best))
-                    best = q;
-        total += time(best);
+        ph.tile_n = kPair == 2 && time(128, 1) < time(T::kTile, 1) ? 128 : T::kTile;
+        if (ph.sym && T::tiles(run.m, ph) * run.batch < groups)
+            for (int tile_n = T::kTile; tile_n >= 128; tile_n /= 2)
+                for (int q = 2; q <= kMaxSplits && q <= blocks / kSplitBlocks; ++q) {
+                    Phase half = ph;
+                    half.tile_n = tile_n;
+                    const size_t units = static_cast<size_t>(T::tiles(run.m, half)) * run.batch * q;
+                    if (units * unit_bytes <= partial_bytes && num + 3 < kMaxPhases &&
+                        time(tile_n, q) < time(ph.tile_n, best)) {
+                        best = q;
+                        ph.tile_n = tile_n;
+                    }
+                }
+        total += time(ph.tile_n, best);
+        const int tiles = T::tiles(run.m, ph) * run.batch;
         // the parts of two products beside each other would share the partials' memory
         if (i > 0 && (best > 1 || split)) ph.after[0] = static_cast<int16_t>(i - 1), ph.after[1] = -1;
         split = best > 1;
@@ -1713,7 +1742,7 @@ double plan(const PhaseList& list, const OrthRun& run, int groups, size_t partia
             sum.after[0] = static_cast<int16_t>(num - 1);
             sum.after[1] = -1;
             sum.first = 0;
-            taken = tiles * T::kTileSlabs;
+            taken = tiles * T::slabs(sum);
             if (out != nullptr) out->phases[num] = sum;
             index[i] = num++;
         }
@@ -1862,79 +1891,94 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& a, bool bf16, cudaStre
 
     // The list of products.  With f the identity's factor, X <- f X + R X where R is the rest of
     // the polynomial of one step (R = B, f = a) or of a group of them.
-    PhaseList list = {};
-    uint8_t free_squares[kSquares];
-    int num_free = 0;
-    for (int i = (grouped > 1 ? kSquares : 2) - 1; i > 0; --i) free_squares[num_free++] = static_cast<uint8_t>(kSquare0 + i);
-    auto take = [&] { return free_squares[--num_free]; };
-    auto give = [&](uint8_t id) { free_squares[num_free++] = id; };
-    const uint8_t A = kSquare0;
     const int m = run.m, n = static_cast<int>(l.n);
     const float ca = a.coef[0];
-    int x = 0;
-    for (int s = 0; s < a.steps; x ^= 1) {
-        const int size = s == 0 ? grouped : 1;
-        const uint8_t hi = static_cast<uint8_t>(kHi0 + x), lo = static_cast<uint8_t>(kLo0 + x);
-        // A = X X^T
-        list.square(hi, hi, kNone, kNone, A, m, n, kGramScale / (p.x_scale * p.x_scale), 0.0f, 0.0f);
-        uint8_t R = kNone;
-        float f = ca;
-        for (int i = 0; i < size; ++i) {
-            const bool more = i + 1 < size;
-            const uint8_t B = take();   // B = b A + c A A
-            list.square(A, A, A, kNone, B, m, m, a.coef[2] / kGramScale, a.coef[1], 0.0f);
-            const int16_t poly = list.last();
-            uint8_t next = B;
-            int16_t rest = poly;
-            if (R != kNone) {           // (a I + B) (f I + R) - a f I = a R + f B + B R
-                next = take();
-                list.square(B, R, R, B, next, m, m, 1.0f / kGramScale, ca, f);
-                f *= ca;
-                rest = list.last();
+    auto build = [&](PhaseList& list, int grouped) {
+        list.num = 0;
+        uint8_t free_squares[kSquares];
+        int num_free = 0;
+        for (int i = (grouped > 1 ? kSquares : 2) - 1; i > 0; --i) free_squares[num_free++] = static_cast<uint8_t>(kSquare0 + i);
+        auto take = [&] { return free_squares[--num_free]; };
+        auto give = [&](uint8_t id) { free_squares[num_free++] = id; };
+        const uint8_t A = kSquare0;
+        int x = 0;
+        for (int s = 0; s < a.steps; x ^= 1) {
+            const int size = s == 0 ? grouped : 1;
+            const uint8_t hi = static_cast<uint8_t>(kHi0 + x), lo = static_cast<uint8_t>(kLo0 + x);
+            // A = X X^T
+            list.square(hi, hi, kNone, kNone, A, m, n, kGramScale / (p.x_scale * p.x_scale), 0.0f, 0.0f);
+            uint8_t R = kNone;
+            float f = ca;
+            for (int i = 0; i < size; ++i) {
+                const bool more = i + 1 < size;
+                const uint8_t B = take();   // B = b A + c A A
+                list.square(A, A, A, kNone, B, m, m, a.coef[2] / kGramScale, a.coef[1], 0.0f);
+                const int16_t poly = list.last();
+                uint8_t next = B;
+                int16_t rest = poly;
+                if (R != kNone) {           // (a I + B) (f I + R) - a f I = a R + f B + B R
+                    next = take();
+                    list.square(B, R, R, B, next, m, m, 1.0f / kGramScale, ca, f);
+                    f *= ca;
+                    rest = list.last();
+                }
+                if (more) {                 // A <- (a I + B) A (a I + B); beside the product above
+                    const uint8_t T = take();
+                    list.square(B, A, A, kNone, T, m, m, 1.0f / kGramScale, ca, 0.0f);
+                    list.after(poly);
+                    list.square(T, B, T, kNone, A, m, m, 1.0f / kGramScale, ca, 0.0f);
+                    list.after(static_cast<int16_t>(list.last() - 1), rest);
+                    give(T);
+                }
+                if (R != kNone) {
+                    give(R);
+                    give(B);
+                }
+                R = next;
             }
-            if (more) {                 // A <- (a I + B) A (a I + B); beside the product above
-                const uint8_t T = take();
-                list.square(B, A, A, kNone, T, m, m, 1.0f / kGramScale, ca, 0.0f);
-                list.after(poly);
-                list.square(T, B, T, kNone, A, m, m, 1.0f / kGramScale, ca, 0.0f);
-                list.after(static_cast<int16_t>(list.last() - 1), rest);
-                give(T);
-            }
-            if (R != kNone) {
-                give(R);
-                give(B);
-            }
-            R = next;
+            s += size;
+            // X = f X + R X
+            Phase ph = {};
+            const bool last = s == a.steps && direct;
+            const float out = last ? 1.0f / p.x_scale : 1.0f;
+            ph.a = R;
+            ph.b = ph.src1 = hi;
+            ph.src2 = lo;
+            ph.dst = last ? static_cast<uint8_t>(kOut) : static_cast<uint8_t>(kHi0 + (x ^ 1));
+            ph.dst_lo = last ? kNone : static_cast<uint8_t>(kLo0 + (x ^ 1));
+            ph.result = !last ? kState : tall ? kBf16Transposed : kBf16;
+            ph.b_along_n = true;
+            ph.n = n;
+            ph.k = m;
+            ph.f_acc = out / kGramScale;
+            ph.f1 = out * f;
+            ph.f2 = ph.f1 / kLoScale;
+            list.add(ph);
+            give(R);
         }
-        s += size;
-        // X = f X + R X
-        Phase ph = {};
-        const bool last = s == a.steps && direct;
-        const float out = last ? 1.0f / p.x_scale : 1.0f;
-        ph.a = R;
-        ph.b = ph.src1 = hi;
-        ph.src2 = lo;
-        ph.dst = last ? static_cast<uint8_t>(kOut) : static_cast<uint8_t>(kHi0 + (x ^ 1));
-        ph.dst_lo = last ? kNone : static_cast<uint8_t>(kLo0 + (x ^ 1));
-        ph.result = !last ? kState : tall ? kBf16Transposed : kBf16;
-        ph.b_along_n = true;
-        ph.n = n;
-        ph.k = m;
-        ph.f_acc = out / kGramScale;
-        ph.f1 = out * f;
-        ph.f2 = ph.f1 / kLoScale;
-        list.add(ph);
-        give(R);
-    }
+        return x;   // which of the state's two places holds the result
+    };
 
-    // The tile that the time model below prefers
-    const double t1 = plan<1>(list, run, limits.single, l.partial_bytes, nullptr);
-    const double t2 = plan<2>(list, run, limits.pairs, l.partial_bytes, nullptr);
-    if (t2 < t1) {
-        plan<2>(list, run, limits.pairs, l.partial_bytes, &run);
+    // The grouping and the tiles that the time model prefers
+    static thread_local PhaseList lists[2];
+    int best_list = 0, best_pair = 1, x = 0;
+    double best = 0.0;
+    for (int i = 0; i < (grouped > 1 ? 2 : 1); ++i) {
+        const int end = build(lists[i], i == 0 ? 1 : grouped);
+        const double t1 = plan<1>(lists[i], run, limits.single, l.partial_bytes, nullptr);
+        const double t2 = plan<2>(lists[i], run, limits.pairs, l.partial_bytes, nullptr);
+        const double t = t2 < t1 ? t2 : t1;
+        if (i > 0 && t >= best) continue;
+        best = t;
+        best_list = i;
+        best_pair = t2 < t1 ? 2 : 1;
+        x = end;
+    }
+    if (best_pair == 2) {
+        plan<2>(lists[best_list], run, limits.pairs, l.partial_bytes, &run);
         e = launch_run<2>(run, limits.pairs, stream);
     } else {
-        plan<1>(list, run, limits.single, l.partial_bytes, &run);
+        plan<1>(lists[best_list], run, limits.single, l.partial_bytes, &run);
         e = launch_run<1>(run, limits.single, stream);
     }
     if (e != cudaSuccess || direct) return e;
