@@ -75,6 +75,14 @@ def _ids(t, name, n, dev):
     return _vector(t, name, n, _IDS, dev), 64 if t.dtype == torch.int64 else 32
 
 
+def _id_array(t, dev):
+    """Pointer, bits and number of token ids of any shape."""
+    _cuda(t, "ids", _IDS, dev)
+    if not t.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    return t.data_ptr(), 64 if t.dtype == torch.int64 else 32, t.numel()
+
+
 def _dt(t):
     return _BF16 if t.dtype == torch.bfloat16 else _F32
 
@@ -150,7 +158,7 @@ def token_logprobs_grad(logits, targets, lse, d_logp, *, entropy=None, d_entropy
             raise ValueError("out must have the logits' shape")
     _call(lib.spl_token_logprobs_grad, dev, logits.data_ptr(), _dt(logits), rows, vocab, stride,
           ids, bits, scale, _vector(lse, "lse", rows, f32, dev), gp, ep, hp, out.data_ptr(),
-          _rows(out, "out"), _flags_ptr(flags, dev))
+          _rows(out, "out"), None if flags is None else _flags_ptr(flags, dev))
     return out
 
 
@@ -163,9 +171,7 @@ def embedding(ids, table, *, scale: float = 1.0, out=None, flags=None):
     stride = _rows(table, "table")
     vocab, width = table.shape
     dev = table.device
-    _cuda(ids, "ids", _IDS, dev)
-    n = ids.numel()
-    id_ptr, bits = _ids(ids, "ids", n, dev)
+    id_ptr, bits, n = _id_array(ids, dev)
     out_stride = width
     if out is None:
         out = torch.empty((*ids.shape, width), dtype=table.dtype, device=dev)
@@ -176,7 +182,7 @@ def embedding(ids, table, *, scale: float = 1.0, out=None, flags=None):
         if out.dim() == 2:
             out_stride = _rows(out, "out")
     _call(lib.spl_embedding, dev, id_ptr, bits, n, table.data_ptr(), _dt(table), vocab, width,
-          stride, scale, out.data_ptr(), out_stride, _flags_ptr(flags, dev))
+          stride, scale, out.data_ptr(), out_stride, None if flags is None else _flags_ptr(flags, dev))
     return out
 
 
@@ -191,15 +197,14 @@ def embedding_grad(ids, d_out, vocab: int, *, scale: float = 1.0, padding_id: in
     lib = library()
     _cuda(d_out, "d_out", _DENSE)
     dev = d_out.device
-    _cuda(ids, "ids", _IDS, dev)
-    n, width = ids.numel(), d_out.shape[-1]
+    id_ptr, bits, n = _id_array(ids, dev)
+    width = d_out.shape[-1]
     if d_out.shape != (*ids.shape, width):
         raise ValueError("d_out must be [*ids.shape, width]")
     if d_out.dim() != 2:
         if not d_out.is_contiguous():
             raise ValueError("d_out must be contiguous unless 2-D")
         d_out = d_out.reshape(n, width)
-    id_ptr, bits = _ids(ids, "ids", n, dev)
     vocab, out_stride = int(vocab), width
     if out is None:
         if accumulate:
@@ -214,7 +219,7 @@ def embedding_grad(ids, d_out, vocab: int, *, scale: float = 1.0, padding_id: in
     workspace = _workspace(workspace, need, dev)
     _call(lib.spl_embedding_grad, dev, id_ptr, bits, n, d_out.data_ptr(), _dt(d_out), width,
           _rows(d_out, "d_out"), vocab, scale, padding_id, int(bool(accumulate)), out.data_ptr(),
-          out_stride, workspace.data_ptr(), need, _flags_ptr(flags, dev))
+          out_stride, workspace.data_ptr(), need, None if flags is None else _flags_ptr(flags, dev))
     return out
 
 
@@ -269,5 +274,5 @@ def orthogonalize(update, *, momentum=None, mu: float = 0.95, nesterov: bool = T
     _call(lib.spl_orthogonalize, dev, update.data_ptr(), _dt(update), batch, rows, cols,
           row_stride, batch_stride, mom, mu, int(bool(nesterov)), steps,
           (ctypes.c_float * 3)(*coefficients), eps, out.data_ptr(), workspace.data_ptr(), need,
-          _flags_ptr(flags, dev))
+          None if flags is None else _flags_ptr(flags, dev))
     return out

@@ -630,9 +630,8 @@ cudaError_t launch_embedding_grad(const EmbeddingGradArgs& a, bool bf16, cudaStr
     const GradLayout l = grad_layout(a.count, a.vocab, a.width);
     unsigned char* ws = static_cast<unsigned char*>(a.workspace);
     auto words = [&](size_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     const bool zero = !a.accumulate, radix = a.count > kRankTokens;
     // Zeroing the whole table beside the sort writes the tokens' rows twice; with many tokens it

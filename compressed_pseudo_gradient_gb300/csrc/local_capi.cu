@@ -1,6 +1,7 @@
 // C ABI of the local step's operators (declared in include/spl_local.h): argument checks on the
 // host, then stream-ordered kernel launches.  Nothing here allocates device memory or
 // synchronises.
+#include <atomic>
 #include <cmath>
 
 #include "capi_util.h"
@@ -47,6 +48,25 @@ bool disjoint(const Range* outs, int num_outs, const Range* ins, int num_ins) {
 bool fits(size_t rows, size_t stride) { return rows <= kMaxDim && stride <= (size_t{1} << 40) / (rows > 0 ? rows : 1) * 64; }
 
 }  // namespace
+
+namespace spl {
+
+cudaError_t sm_count(int* sms) {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    *sms = cached[dev].load(std::memory_order_relaxed);
+    if (*sms == 0) {
+        e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        cached[dev].store(*sms, std::memory_order_relaxed);
+    }
+    return cudaSuccess;
+}
+
+}  // namespace spl
 
 extern "C" {
 

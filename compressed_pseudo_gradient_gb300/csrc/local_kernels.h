@@ -13,6 +13,9 @@ struct TokenIds {
     bool wide;
 };
 
+// The current device's SM count, asked for once per device.
+cudaError_t sm_count(int* sms);
+
 constexpr int kMaxTop = 32;   // alternatives per row: one list entry per lane of a warp
 
 struct LogprobsArgs {

@@ -665,9 +665,8 @@ k_logprobs_grad(const __grid_constant__ LogprobsGradArgs a, int parts, bool vect
 
 template <bool kBf16, bool kTop>
 cudaError_t launch_forward(const LogprobsArgs& a, cudaStream_t stream) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     int parts = 1;
     while (parts < kMaxParts && a.rows * parts < 4 * sms && a.vocab / (2 * parts) >= 2048) parts *= 2;

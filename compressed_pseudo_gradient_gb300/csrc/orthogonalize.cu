@@ -1305,31 +1305,48 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
                 // this CTA adds up its share of the rows and gives the result to all
                 const int r0 = kBlock * static_cast<int>(cta) / static_cast<int>(ctas),
                           r1 = kBlock * (static_cast<int>(cta) + 1) / static_cast<int>(ctas);
-                for (int i = tid; i < (r1 - r0) * 32; i += kSmallThreads) {
-                    const int r = r0 + i / 32, c = i % 32;
-                    const float4* from = reinterpret_cast<const float4*>(other) + r * 32 + (c ^ (r & 31));
-                    float4 q[kSmallClusters];
+                // kItems places at once from each of at most kMost CTAs: 16 loads in flight
+                auto add_up = [&](auto items, auto most) {
+                    constexpr int kItems = decltype(items)::value, kMost = decltype(most)::value;
+                    const int total = (r1 - r0) * 32;
+                    for (int i0 = tid; i0 < total; i0 += kSmallThreads * kItems) {
+                        float4 q[kItems][kMost];
 #pragma unroll
-                    for (int k = 0; k < kSmallClusters; ++k)
-                        if (k < static_cast<int>(ctas))
-                            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                         : "=f"(q[k].x), "=f"(q[k].y), "=f"(q[k].z), "=f"(q[k].w)
-                                         : "r"(remote_addr(from, k)));
-                    float4 t = q[0];
+                        for (int j = 0; j < kItems; ++j) {
+                            const int i = i0 + j * kSmallThreads, r = r0 + i / 32, c = i % 32;
+                            if (i >= total) continue;
+                            const float4* from = reinterpret_cast<const float4*>(other) + r * 32 + (c ^ (r & 31));
 #pragma unroll
-                    for (int k = 1; k < kSmallClusters; ++k) {
-                        if (k >= static_cast<int>(ctas)) continue;
-                        t.x = __fadd_rn(t.x, q[k].x), t.y = __fadd_rn(t.y, q[k].y);
-                        t.z = __fadd_rn(t.z, q[k].z), t.w = __fadd_rn(t.w, q[k].w);
+                            for (int k = 0; k < kMost; ++k)
+                                if (k < static_cast<int>(ctas))
+                                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                                 : "=f"(q[j][k].x), "=f"(q[j][k].y), "=f"(q[j][k].z), "=f"(q[j][k].w)
+                                                 : "r"(remote_addr(from, k)));
+                        }
+#pragma unroll
+                        for (int j = 0; j < kItems; ++j) {
+                            const int i = i0 + j * kSmallThreads, r = r0 + i / 32, c = i % 32;
+                            if (i >= total) continue;
+                            float4 t = q[j][0];
+#pragma unroll
+                            for (int k = 1; k < kMost; ++k) {
+                                if (k >= static_cast<int>(ctas)) continue;
+                                t.x = __fadd_rn(t.x, q[j][k].x), t.y = __fadd_rn(t.y, q[j][k].y);
+                                t.z = __fadd_rn(t.z, q[j][k].z), t.w = __fadd_rn(t.w, q[j][k].w);
+                            }
+                            const __half2 h0 = __floats2half2_rn(__fmul_rn(t.x, gram_scale), __fmul_rn(t.y, gram_scale));
+                            const __half2 h1 = __floats2half2_rn(__fmul_rn(t.z, gram_scale), __fmul_rn(t.w, gram_scale));
+                            const unsigned char* to =
+                                a_op + c / 16 * kBlockBytes + swizzled(r, c % 16 / 2) + c % 2 * 8;
+                            for (uint32_t k = 0; k < ctas; ++k)
+                                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};"
+                                             ::"r"(remote_addr(to, k)), "r"(*reinterpret_cast<const uint32_t*>(&h0)),
+                                               "r"(*reinterpret_cast<const uint32_t*>(&h1)) : "memory");
+                        }
                     }
-                    const __half2 h0 = __floats2half2_rn(__fmul_rn(t.x, gram_scale), __fmul_rn(t.y, gram_scale));
-                    const __half2 h1 = __floats2half2_rn(__fmul_rn(t.z, gram_scale), __fmul_rn(t.w, gram_scale));
-                    const unsigned char* to = a_op + c / 16 * kBlockBytes + swizzled(r, c % 16 / 2) + c % 2 * 8;
-                    for (uint32_t k = 0; k < ctas; ++k)
-                        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};"
-                                     ::"r"(remote_addr(to, k)), "r"(*reinterpret_cast<const uint32_t*>(&h0)),
-                                       "r"(*reinterpret_cast<const uint32_t*>(&h1)) : "memory");
-                }
+                };
+                if (ctas <= 4) add_up(Count<4>(), Count<4>());
+                else add_up(Count<1>(), Count<kSmallClusters>());
             }
         }
         publish();
