@@ -129,8 +129,10 @@ __device__ __forceinline__ void zero_table(const ZeroTable& z, int64_t cta, int6
 }
 
 // Few tokens: a token's place is the number of tokens that sort before it, counted against all
-// keys in shared memory by kRankLanes threads.  No step waits for another CTA: SMALLSORT us.
-constexpr int kRankTokens = 8192;    // most tokens sorted this way
+// keys in shared memory by kRankLanes threads.  No step waits for another CTA, but the work grows
+// with the square: the whole accumulating call takes 24 us for 4,096 tokens of width 1024 (37 us
+// with the radix sort below) and 45 us for 8,192 (42 us).
+constexpr int kRankTokens = 4096;    // most tokens sorted this way
 constexpr int kRankThreads = 256;
 constexpr int kRankLanes = 8;
 
@@ -166,7 +168,7 @@ k_sort_rank(const __grid_constant__ SortArgs p, const __grid_constant__ ZeroTabl
 // kernel.  A CTA has one tile of consecutive entries, a warp a consecutive share of it, so ranks
 // by (tile, warp, round, lane) keep equal digits in order.  Per pass: every warp counts its
 // digits, the tiles' counts go to memory, and after a barrier over the sorting CTAs each adds up
-// for itself what lies before its own entries.  65,536 tokens: SORTBIG us.
+// for itself what lies before its own entries.  65,536 tokens of 19-bit ids: 27 us in two passes.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 10;
@@ -298,13 +300,14 @@ k_sort_radix(const __grid_constant__ SortArgs p, const __grid_constant__ ZeroTab
 }
 
 // ---- sums -----------------------------------------------------------------------------------
-// Sorted tokens per window.  Short windows give few tokens enough CTAs (2,000 tokens of width
-// 1001: SMALLWIN us with 16, 6 us with 64); long ones leave fewer partial sums.
+// Sorted tokens per window.  Short windows give small gradients enough CTAs (2,000 tokens of
+// width 1001: 32 us for the call with windows of 16, 45 us with 64); long ones leave fewer partial
+// sums (16,384 of width 4096: 161 against 132 us; 32,768 of width 512: 138 against 125 us).
 constexpr int kWindow = 64;
 constexpr int kShortWindow = 16;
-constexpr int kShortWindowTokens = 16384;   // up to this many tokens
+constexpr int64_t kShortWindowValues = int64_t{1} << 23;   // up to this many values of d_out
 
-int window_of(int64_t count) { return count <= kShortWindowTokens ? kShortWindow : kWindow; }
+int window_of(int64_t count, int64_t width) { return count * width <= kShortWindowValues ? kShortWindow : kWindow; }
 
 struct GradSums {
     const uint32_t* keys;   // sorted ids
@@ -517,7 +520,8 @@ constexpr int kMaxTiles = 256;   // sorting CTAs; at most one per SM
 
 GradLayout grad_layout(int64_t count, int64_t vocab, int64_t width) {
     GradLayout l;
-    l.windows = static_cast<uint32_t>((count + window_of(count) - 1) / window_of(count));
+    const int window = window_of(count, width);
+    l.windows = static_cast<uint32_t>((count + window - 1) / window);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -635,7 +639,8 @@ cudaError_t launch_embedding_grad(const EmbeddingGradArgs& a, bool bf16, cudaStr
     if (e != cudaSuccess) return e;
     const bool zero = !a.accumulate, radix = a.count > kRankTokens;
     // Zeroing the whole table beside the sort writes the tokens' rows twice; with many tokens it
-    // is left to the summing kernel, which knows them from the bitmap.
+    // is left to the summing kernel, which knows them from the bitmap (16,384 tokens of width 1024,
+    // 32,768 ids: 54 us beside the sort, 62 us after it; 32,768 tokens of width 2048: 145 and 136).
     const bool zero_all = zero && (!radix || a.count * a.width <= (int64_t{1} << 25));
     SortArgs p = {};
     p.ids = a.ids;
@@ -672,7 +677,7 @@ cudaError_t launch_embedding_grad(const EmbeddingGradArgs& a, bool bf16, cudaStr
     g.n = p.n;
     g.vocab = p.vocab;
     g.windows = l.windows;
-    g.window = static_cast<uint32_t>(window_of(a.count));
+    g.window = static_cast<uint32_t>(window_of(a.count, a.width));
     g.scale = a.scale;
     g.accumulate = a.accumulate;
     const bool vec = on16(a.d_out, a.d_out_stride, bf16 ? 2 : 4) && on16(a.d_table, a.stride, 4) &&

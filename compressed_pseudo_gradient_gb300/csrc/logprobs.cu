@@ -18,7 +18,7 @@
 // which are ranked as 64-bit keys (the value's ordered bits, then the complement of its index:
 // equal values rank by lower index), sorted and merged 32 at a time in a warp's lanes.  A row with
 // too many values at the bound (ties, few unmasked values) is read again in full instead.
-// 4096 x 262,208 bf16 with 5 alternatives: LISTTIME; 0.308 ms with none.
+// 4096 x 262,208 bf16 with 5 alternatives: 0.354 ms; with none 0.314 ms, 6.8 TB/s.
 #include <cooperative_groups.h>
 
 #include "local_device.cuh"
@@ -252,7 +252,9 @@ struct Group {
     }
 };
 
-// Bound: HBM (about 5 instructions per value, one of them an exponential).
+// Bound: HBM (about 5 instructions per value, one of them an exponential), with alternatives also
+// by the barriers and sorts at a row's end.  Four CTAs of 256 threads per SM, four 16-byte loads in
+// flight per thread while the four before them are added.
 template <bool kBf16, bool kTop>
 __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const __grid_constant__ LogprobsArgs a,
                                                           int parts) {
@@ -521,9 +523,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const __grid_constant_
 }
 
 // ---- gradient -------------------------------------------------------------------------------
-// Bound: HBM, every logit read once and every gradient written once.  A CTA takes kGradVecs
-// vectors of a row per thread; rows whose input and output sit differently within 16 bytes are
-// taken value by value.
+// Bound: HBM, every logit read once and every gradient written once: 4096 x 262,208 bf16 0.62 ms,
+// 7.0 TB/s.  A CTA takes kGradVecs vectors of a row per thread; rows whose input and output sit
+// differently within 16 bytes are taken value by value.
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;
 
@@ -668,8 +670,14 @@ cudaError_t launch_forward(const LogprobsArgs& a, cudaStream_t stream) {
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
+    // A row is split while the parts still have an SM each and at least 16 KB.  One CTA streams a
+    // row at about 40 GB/s: one row of 262,208 bf16 takes 13.2 us whole (20.3 us with 8
+    // alternatives), 4.6 us (9.1) in 16 parts; 16 such rows 13.6 against 6.6 us in 8 parts.  With
+    // as many rows as SMs a cluster only adds its barriers: 150 rows 16.7 us whole, 19.5 us in 4
+    // parts; 64 rows of 32,768 4.3 against 9.4 us in 8.
+    const int64_t row_bytes = a.vocab * Vec16<kBf16>::kBytes;
     int parts = 1;
-    while (parts < kMaxParts && a.rows * parts < 4 * sms && a.vocab / (2 * parts) >= 2048) parts *= 2;
+    while (parts < kMaxParts && a.rows * (2 * parts) <= sms && row_bytes / (2 * parts) >= 16384) parts *= 2;
     if (parts > 8) {   // beyond the portable cluster size
         e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&k_logprobs<kBf16, kTop>),
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

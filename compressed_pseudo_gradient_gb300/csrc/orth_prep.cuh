@@ -1,0 +1,277 @@
+// Orthogonalised update: the momentum step, the norm and the state's first value (see
+// orthogonalize.cu for the method and the number formats).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "local_device.cuh"
+#include "local_kernels.h"
+
+namespace spl {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kGramScale = 1024.0f;    // of A and B
+constexpr float kLoScale = 2048.0f;      // of the state's low plane
+
+constexpr int kPrepThreads = 256;
+constexpr int kMaxPartials = 1216;  // sums of squares per matrix: eight CTAs per SM
+constexpr int kMaxPhases = 160;     // of the run kernel below
+constexpr int kMaxSlots = 32;       // of matrices with counters of their own
+
+struct PrepArgs {
+    const void* update;
+    int64_t rows, cols, row_stride, batch_stride;
+    float* momentum;
+    float mu;
+    bool nesterov;
+    float eps, x_scale;
+    double* partials;   // [batch][kMaxPartials]
+    int num_partials;
+    __half* hi;         // [batch][m][ld]
+    __half* lo;
+    int64_t ld, plane;  // plane = m * ld
+    uint32_t* arrived;  // the run kernel's phase counters, cleared here
+    uint32_t* flags;
+};
+
+// u of one entry once the momentum holds its new value.
+__device__ __forceinline__ float step_value(float g, float m, const PrepArgs& p) {
+    if (p.momentum == nullptr) return g;
+    return p.nesterov ? __fmaf_rn(p.mu, m, g) : m;
+}
+
+// A matrix as a flat range of units (16-byte vectors of the update where its rows allow, single
+// values otherwise): a CTA takes kPrepUnits per thread at a time, so that short rows share a CTA.
+constexpr int kPrepUnits = 4;
+
+template <bool kBf16, bool kVec>
+struct PrepUnit {
+    static constexpr int kN = kVec ? Vec16<kBf16>::kN : 1;
+    float x[kN];
+
+    __device__ __forceinline__ void load(const PrepArgs& p, int64_t b, int64_t r, int64_t u) {
+        const unsigned char* row = static_cast<const unsigned char*>(p.update) +
+                                   (b * p.batch_stride + r * p.row_stride) * Vec16<kBf16>::kBytes;
+        if constexpr (kVec) Vec16<kBf16>::unpack(reinterpret_cast<const uint4*>(row)[u], x);
+        else x[0] = Vec16<kBf16>::load1(row, u);
+    }
+    __device__ __forceinline__ void load_momentum(const float* m) {
+        if constexpr (kVec) {
+#pragma unroll
+            for (int i = 0; i < kN; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(m + i);
+                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+            }
+        } else {
+            x[0] = *m;
+        }
+    }
+    __device__ __forceinline__ void store_momentum(float* m) const {
+        if constexpr (kVec) {
+#pragma unroll
+            for (int i = 0; i < kN; i += 4)
+                *reinterpret_cast<float4*>(m + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        } else {
+            *m = x[0];
+        }
+    }
+};
+
+// The momentum step and each CTA's share of |u|^2.
+template <bool kBf16, bool kVec>
+__global__ void __launch_bounds__(kPrepThreads) k_orth_norm(const __grid_constant__ PrepArgs p) {
+    using U = PrepUnit<kBf16, kVec>;
+    __shared__ double s_sum[kPrepThreads / 32];
+    const int64_t b = blockIdx.y;
+    if (blockIdx.x == 0 && b == 0)
+        for (int i = threadIdx.x; i < kMaxPhases * kMaxSlots; i += kPrepThreads) p.arrived[i] = 0;
+    const uint32_t per_row = static_cast<uint32_t>(p.cols / U::kN);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPrepThreads * kPrepUnits);
+    double total = 0.0;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kPrepThreads * kPrepUnits);
+         first < p.rows * per_row; first += step) {
+        const int64_t row0 = first / per_row;
+        const uint32_t rem0 = static_cast<uint32_t>(first - row0 * per_row);
+        U g[kPrepUnits], m[kPrepUnits];
+        int64_t at[kPrepUnits];
+#pragma unroll
+        for (int k = 0; k < kPrepUnits; ++k) {
+            const uint32_t i = rem0 + k * kPrepThreads + threadIdx.x;
+            const int64_t r = row0 + i / per_row;
+            at[k] = -1;
+            if (r >= p.rows || !SPL_CHECK(r < p.rows, kSiteOrthIn, r)) continue;
+            const uint32_t u = i % per_row;
+            g[k].load(p, b, r, u);
+            at[k] = (b * p.rows + r) * p.cols + static_cast<int64_t>(u) * U::kN;
+            if (p.momentum != nullptr) m[k].load_momentum(p.momentum + at[k]);
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kPrepUnits; ++k) {
+            if (at[k] < 0) continue;
+#pragma unroll
+            for (int i = 0; i < U::kN; ++i) {
+                if (p.momentum != nullptr) m[k].x[i] = __fmaf_rn(p.mu, m[k].x[i], g[k].x[i]);
+                const float u = step_value(g[k].x[i], m[k].x[i], p);
+                sum = __fmaf_rn(u, u, sum);
+            }
+            if (p.momentum != nullptr) m[k].store_momentum(p.momentum + at[k]);
+        }
+        total += static_cast<double>(sum);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(kAll, total, off);
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kPrepThreads / 32; ++w) total += s_sum[w];
+        p.partials[b * kMaxPartials + blockIdx.x] = total;
+    }
+}
+
+// x_scale / (|u| + eps) of matrix b, the same in every thread of the CTA.
+__device__ __forceinline__ float state_factor(const PrepArgs& p, int64_t b) {
+    __shared__ double s_sum[kPrepThreads / 32];
+    __shared__ float s_factor;
+    double total = 0.0;
+    for (int i = threadIdx.x; i < p.num_partials; i += kPrepThreads)
+        total += p.partials[b * kMaxPartials + i];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(kAll, total, off);
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kPrepThreads / 32; ++w) total += s_sum[w];
+        const float norm = static_cast<float>(sqrt(total));
+        s_factor = __fdiv_rn(p.x_scale, __fadd_rn(norm, p.eps));
+        if (!(norm <= 3.402823466e+38f)) {
+            s_factor = __uint_as_float(0x7fc00000u);
+            if (p.flags != nullptr) atomicOr(p.flags, kFlagNonFinite);
+        }
+    }
+    __syncthreads();
+    return s_factor;
+}
+
+__device__ __forceinline__ float nan_value() { return __uint_as_float(0x7fc00000u); }
+
+__device__ __forceinline__ void split_state(float x, __half& hi, __half& lo) {
+    hi = __float2half_rn(x);
+    lo = __float2half_rn(__fmul_rn(__fsub_rn(x, __half2float(hi)), kLoScale));
+}
+
+// kN consecutive values of the state's two planes.
+template <int kN>
+__device__ __forceinline__ void store_state(const PrepArgs& p, int64_t at, const float* x) {
+    __half h[kN], l[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) split_state(x[i], h[i], l[i]);
+    if constexpr (kN == 8) {
+        *reinterpret_cast<uint4*>(p.hi + at) = *reinterpret_cast<const uint4*>(h);
+        *reinterpret_cast<uint4*>(p.lo + at) = *reinterpret_cast<const uint4*>(l);
+    } else if constexpr (kN == 4) {
+        *reinterpret_cast<uint2*>(p.hi + at) = *reinterpret_cast<const uint2*>(h);
+        *reinterpret_cast<uint2*>(p.lo + at) = *reinterpret_cast<const uint2*>(l);
+    } else {
+        p.hi[at] = h[0];
+        p.lo[at] = l[0];
+    }
+}
+
+// X = u / (|u| + eps) in the state's format.
+template <bool kBf16, bool kVec>
+__global__ void __launch_bounds__(kPrepThreads) k_orth_state(const __grid_constant__ PrepArgs p) {
+    using U = PrepUnit<kBf16, kVec>;
+    const int64_t b = blockIdx.y;
+    const float f = state_factor(p, b);
+    const uint32_t per_row = static_cast<uint32_t>(p.cols / U::kN);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPrepThreads * kPrepUnits);
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kPrepThreads * kPrepUnits);
+         first < p.rows * per_row; first += step) {
+        const int64_t row0 = first / per_row;
+        const uint32_t rem0 = static_cast<uint32_t>(first - row0 * per_row);
+        U g[kPrepUnits], m[kPrepUnits];
+        int64_t at[kPrepUnits];
+#pragma unroll
+        for (int k = 0; k < kPrepUnits; ++k) {
+            const uint32_t i = rem0 + k * kPrepThreads + threadIdx.x;
+            const int64_t r = row0 + i / per_row;
+            at[k] = -1;
+            if (r >= p.rows || !SPL_CHECK(r < p.rows, kSiteOrthIn, r)) continue;
+            const uint32_t u = i % per_row;
+            g[k].load(p, b, r, u);
+            if (p.momentum != nullptr)
+                m[k].load_momentum(p.momentum + (b * p.rows + r) * p.cols + static_cast<int64_t>(u) * U::kN);
+            at[k] = b * p.plane + r * p.ld + static_cast<int64_t>(u) * U::kN;
+        }
+#pragma unroll
+        for (int k = 0; k < kPrepUnits; ++k) {
+            if (at[k] < 0) continue;
+#pragma unroll
+            for (int i = 0; i < U::kN; ++i) g[k].x[i] = __fmul_rn(step_value(g[k].x[i], m[k].x[i], p), f);
+            store_state<U::kN>(p, at[k], g[k].x);
+        }
+    }
+}
+
+// The same for a tall matrix, whose state is its transpose: 64 x 64 tiles through shared memory.
+template <bool kBf16, bool kVec>
+__global__ void __launch_bounds__(kPrepThreads) k_orth_state_tall(const __grid_constant__ PrepArgs p) {
+    using U = PrepUnit<kBf16, kVec>;
+    constexpr int kAcross = 64 / U::kN, kDown = kPrepThreads / kAcross;
+    __shared__ float s_tile[64][65];
+    const int64_t b = blockIdx.y;
+    const float f = state_factor(p, b);
+    const int64_t tiles_r = (p.rows + 63) / 64, tiles = tiles_r * ((p.cols + 63) / 64);
+    const int uc = threadIdx.x % kAcross, ur = threadIdx.x / kAcross;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t r0 = t % tiles_r * 64, c0 = t / tiles_r * 64;
+#pragma unroll
+        for (int k = 0; k < 64 / kDown; ++k) {
+            const int64_t r = r0 + ur + k * kDown, c = c0 + uc * U::kN;
+            if (r >= p.rows || c >= p.cols || !SPL_CHECK(r < p.rows, kSiteOrthIn, r)) continue;
+            U g, m;
+            g.load(p, b, r, c / U::kN);
+            if (p.momentum != nullptr) m.load_momentum(p.momentum + (b * p.rows + r) * p.cols + c);
+#pragma unroll
+            for (int i = 0; i < U::kN; ++i)
+                s_tile[ur + k * kDown][uc * U::kN + i] = __fmul_rn(step_value(g.x[i], m.x[i], p), f);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {   // 8 of the tile's rows per thread: the state's columns
+            const int c = (threadIdx.x >> 3) + 32 * k, r = (threadIdx.x & 7) * 8;
+            if (c0 + c >= p.cols || r0 + r >= p.rows) continue;
+            // columns up to the row pitch, a multiple of 8, are this buffer's own
+            if (!SPL_CHECK(r0 + r + 8 <= p.ld, kSiteOrthState, r0 + r)) continue;
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = s_tile[r + i][c];
+            store_state<8>(p, b * p.plane + (c0 + c) * p.ld + r0 + r, x);
+        }
+        __syncthreads();
+    }
+}
+
+template <bool kBf16, bool kVec>
+cudaError_t launch_prep(PrepArgs p, int64_t batch, bool tall, int sms, cudaStream_t stream) {
+    const int64_t per_cta = static_cast<int64_t>(kPrepThreads) * kPrepUnits;
+    const int64_t ctas = (p.rows * (p.cols / PrepUnit<kBf16, kVec>::kN) + per_cta - 1) / per_cta;
+    p.num_partials = static_cast<int>(ctas < kMaxPartials ? ctas : kMaxPartials);
+    const unsigned b = static_cast<unsigned>(batch);
+    k_orth_norm<kBf16, kVec><<<dim3(static_cast<unsigned>(p.num_partials), b), kPrepThreads, 0, stream>>>(p);
+    const int64_t most = 8 * static_cast<int64_t>(sms);   // as many as are resident, then loop
+    if (tall) {
+        const int64_t tiles = (p.rows + 63) / 64 * ((p.cols + 63) / 64);
+        k_orth_state_tall<kBf16, kVec><<<dim3(static_cast<unsigned>(tiles < most ? tiles : most), b), kPrepThreads,
+                                         0, stream>>>(p);
+    } else {
+        k_orth_state<kBf16, kVec><<<dim3(static_cast<unsigned>(ctas < most ? ctas : most), b), kPrepThreads, 0,
+                                    stream>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace spl

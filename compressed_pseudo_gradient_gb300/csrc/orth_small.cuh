@@ -1,0 +1,443 @@
+// Orthogonalised update: small matrices, the whole call in one cluster (see orthogonalize.cu for
+// the method and the number formats).
+//
+// A matrix whose short side is at most 128 (256: a pair of CTAs, for a long side up to 256) never
+// leaves its cluster: X lies as fp16 operands in shared memory and as fp32 state in tensor memory,
+// each CTA with 256 of its columns.  One launch does the momentum step, the norm, every product and
+// the output, with three barriers a step instead of trips through L2 and waits across the grid.
+//   kPair = 1: 128 rows of X per CTA, the cluster's CTAs side by side along the long side.  Each
+//     multiplies its own columns, the partial Gram matrices are added up (in CTA order) and handed
+//     round through distributed shared memory, and each CTA then forms B and its columns of B X.
+//   kPair = 2: each CTA has 128 of the 256 rows.  Products are the pair's (cta_group::2); a
+//     symmetric matrix's rows serve as both operands, and for B X the CTAs exchange the halves of
+//     X that the other one's columns need.
+// X by rows serves the Gram product (rows along K) and, the same bytes read the other way, B X
+// (rows along N).
+#pragma once
+
+#include "orth_run.cuh"
+
+namespace spl {
+namespace {
+
+constexpr int kSmallThreads = 256;
+constexpr int kSmallCols = 256;                    // of X per CTA
+constexpr int kSmallClusters = 16;
+constexpr int kStagePitch = kSmallCols + 1;        // floats; odd, so rows and columns both read freely
+constexpr int kBlockBytes = kBlock * kTileK * 2;   // 64 columns of an operand
+
+template <int kPair>
+struct SmallShape {
+    static constexpr int kGramCols = kBlock * kPair;
+    static constexpr int kXBytes = kSmallCols / 64 * kBlockBytes;
+    static constexpr int kABytes = kGramCols / 64 * kBlockBytes;
+    // partial sums (kPair = 1), or the columns' half of X in all rows (kPair = 2)
+    static constexpr int kOtherBytes = kPair == 1 ? kBlock * kBlock * 4 : 2 * 2 * kBlockBytes;
+    static constexpr int kUsed = kXBytes + kABytes + kOtherBytes;
+    static constexpr int kStaging = kBlock * kStagePitch * 4;
+    static constexpr int kSmem = (kUsed > kStaging ? kUsed : kStaging) + 1024;
+};
+
+struct SmallArgs {
+    PrepArgs p;
+    uint16_t* out;
+    int m, n, width;    // short and long side; columns of X per CTA (kPair = 1: a multiple of 64)
+    int steps;
+    bool tall;
+    float a, b, c;      // coefficients
+    uint32_t* flags;
+};
+
+__device__ __forceinline__ void tmem_store_32(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+          "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
+          "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+          "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+          "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t remote_addr(const void* p, uint32_t cta) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(cta));
+    return a;
+}
+
+template <int kPair, bool kBf16, bool kVec>
+__global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_constant__ SmallArgs s) {
+    using S = SmallShape<kPair>;
+    using U = PrepUnit<kBf16, kVec>;
+    constexpr int kGramCols = S::kGramCols;
+    constexpr int kPerThread = kSmallCols / 2;   // columns of X per thread: two warps share a row
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* x_op = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char* a_op = x_op + S::kXBytes;
+    unsigned char* other = a_op + S::kABytes;
+    float* staging = reinterpret_cast<float*>(x_op);   // before the operands exist, and after
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ uint32_t s_tmem;
+    __shared__ double s_sum[kSmallThreads / 32 + 1];
+    const PrepArgs& p = s.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t ctas, cta;   // of the cluster
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(cta));
+    const int64_t b = blockIdx.x / ctas;
+    const int row0 = kPair == 2 ? static_cast<int>(cta) * kBlock : 0;        // this CTA's rows of X
+    const int col0 = kPair == 2 ? 0 : static_cast<int>(cta) * s.width;       // and columns
+    const int rows = min(kBlock, s.m - row0), cols = min(s.width, s.n - col0);   // may be <= 0
+    bool late = false;
+
+    if (tid == 0) {
+        mbar_init(&bar, 1);
+        fence_async_smem();
+    }
+    if (warp == 0) {
+        if constexpr (kPair == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                         ::"r"(smem_addr(&s_tmem)), "n"(512) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                         ::"r"(smem_addr(&s_tmem)), "n"(512) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
+    }
+
+    // the update with its momentum step, as fp32 [row][column] in shared memory: a warp per stored
+    // line, kLines of them at a time for the loads in flight
+    const int lines = s.tall ? cols : rows, length = s.tall ? rows : cols;   // as stored
+    const int64_t line0 = s.tall ? col0 : row0, at0 = s.tall ? row0 : col0;
+    constexpr int kWarps = kSmallThreads / 32, kLines = 4;
+    float sum = 0.0f;
+    for (int l0 = warp; l0 < lines; l0 += kWarps * kLines) {
+        for (int at = lane * U::kN; at < length; at += 32 * U::kN) {
+            U g[kLines], mom[kLines];
+#pragma unroll
+            for (int k = 0; k < kLines; ++k) {
+                const int64_t line = line0 + l0 + k * kWarps;
+                if (l0 + k * kWarps >= lines || !SPL_CHECK(line < p.rows, kSiteOrthIn, line)) continue;
+                g[k].load(p, b, line, (at0 + at) / U::kN);
+                if (p.momentum != nullptr) mom[k].load_momentum(p.momentum + (b * p.rows + line) * p.cols + at0 + at);
+            }
+#pragma unroll
+            for (int k = 0; k < kLines; ++k) {
+                const int line = l0 + k * kWarps;
+                if (line >= lines) continue;
+#pragma unroll
+                for (int e = 0; e < U::kN; ++e) {
+                    if (p.momentum != nullptr) mom[k].x[e] = __fmaf_rn(p.mu, mom[k].x[e], g[k].x[e]);
+                    const float u = step_value(g[k].x[e], mom[k].x[e], p);
+                    sum = __fmaf_rn(u, u, sum);
+                    staging[s.tall ? (at + e) * kStagePitch + line : line * kStagePitch + at + e] = u;
+                }
+                if (p.momentum != nullptr)
+                    mom[k].store_momentum(p.momentum + (b * p.rows + line0 + line) * p.cols + at0 + at);
+            }
+        }
+    }
+    double norm2 = static_cast<double>(sum);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) norm2 += __shfl_xor_sync(kAll, norm2, off);
+    if (lane == 0) s_sum[warp] = norm2;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < kSmallThreads / 32; ++w) norm2 += s_sum[w];
+        s_sum[kSmallThreads / 32] = norm2;
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    cluster_barrier();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    norm2 = 0.0;
+    for (uint32_t q = 0; q < ctas; ++q) {
+        double v;
+        asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(remote_addr(&s_sum[kSmallThreads / 32], q)));
+        norm2 += v;
+    }
+    const float norm = static_cast<float>(sqrt(norm2));
+    float factor = __fdiv_rn(p.x_scale, __fadd_rn(norm, p.eps));
+    if (!(norm <= 3.402823466e+38f)) {
+        factor = nan_value();
+        if (tid == 0 && cta == 0 && s.flags != nullptr) atomicOr(s.flags, kFlagNonFinite);
+    }
+
+    // a thread's row, and its half of the columns
+    const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+    const uint32_t lanes = s_tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t state = lanes + kSmallCols;   // X in columns 256 .. 511, accumulators in 0 .. 255
+    // 8 columns of the operand X from column c, and in a pair their copy with the columns' owner
+    auto put_x = [&](int c, const uint4& w) {
+        *reinterpret_cast<uint4*>(x_op + c / 64 * kBlockBytes + swizzled(row, c % 64 / 8)) = w;
+        if constexpr (kPair == 2) {
+            const uint32_t to = remote_addr(other, c / 128) + cta * (2 * kBlockBytes) + c % 128 / 64 * kBlockBytes +
+                                swizzled(row, c % 64 / 8);
+            asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
+                         ::"r"(to), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+        }
+    };
+    // what threads of the cluster wrote to shared memory, before the products read it
+    auto publish = [&] {
+        fence_async_all();
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        if (ctas > 1) cluster_barrier();
+        else __syncthreads();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        fence_async_all();
+    };
+    uint32_t bar_phase = 0;
+    // one product: `issue` runs in the thread that issues it; then all wait for it
+    auto product = [&](auto issue) {
+        if (tid == 0 && (kPair == 1 || cta == 0)) {
+            issue();
+            mma_commit<kPair>(&bar);
+        }
+        __syncwarp();
+        if (!late) late = !mbar_wait(&bar, bar_phase);
+        bar_phase ^= 1u;
+        __syncwarp();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    };
+
+    {
+        float x[kPerThread];
+#pragma unroll
+        for (int c = 0; c < kPerThread; ++c) {
+            const int col = half * kPerThread + c;
+            x[c] = row < rows && col < cols ? __fmul_rn(staging[row * kStagePitch + col], factor) : 0.0f;
+        }
+        if (ctas > 1) cluster_barrier();   // a pair writes to the other's memory below
+        else __syncthreads();
+#pragma unroll
+        for (int c = 0; c < kPerThread; c += 8) put_x(half * kPerThread + c, pack_half8(x + c));
+#pragma unroll
+        for (int c = 0; c < kPerThread; c += 32)
+            tmem_store_32(state + half * kPerThread + c, reinterpret_cast<const uint32_t*>(x) + c);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    }
+    publish();
+
+    const float gram_scale = kGramScale / (p.x_scale * p.x_scale);
+    const int k_x = (kPair == 2 ? s.n : s.width), k_a = s.m;   // lengths of the products
+    constexpr uint32_t kInstr = (1u << 4) | (static_cast<uint32_t>(kGramCols / 16) << 24);   // fp32 sums, M
+    for (int step = 0; step < s.steps; ++step) {
+        // A = X X^T (this CTA's columns)
+        product([&] {
+            constexpr uint32_t idesc = kInstr | (static_cast<uint32_t>(kGramCols / 8) << 17);
+            for (int k = 0; k < k_x; k += 16) {
+                const uint64_t d = operand_desc(x_op + k / 64 * kBlockBytes, 16) + k % 64 / 16 * 2;
+                mma_f16<kPair>(s_tmem, d, d, idesc, k > 0);
+            }
+        });
+        {
+            float v[kGramCols / 2];
+#pragma unroll
+            for (int c = 0; c < kGramCols / 2; c += 32)
+                tmem_load_32(lanes + half * (kGramCols / 2) + c, reinterpret_cast<uint32_t*>(v) + c);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            if (kPair == 2 || ctas == 1) {
+#pragma unroll
+                for (int c = 0; c < kGramCols / 2; c += 8) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[c + i] = __fmul_rn(v[c + i], gram_scale);
+                    const int col = half * (kGramCols / 2) + c;
+                    *reinterpret_cast<uint4*>(a_op + col / 64 * kBlockBytes + swizzled(row, col % 64 / 8)) = pack_half8(v + c);
+                }
+            } else {   // partial sums: chunk c of row r at place c ^ (r & 31)
+                float4* mine = reinterpret_cast<float4*>(other) + row * 32;
+#pragma unroll
+                for (int c = 0; c < kGramCols / 2; c += 4)
+                    mine[((half * (kGramCols / 2) + c) / 4) ^ (row & 31)] = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                cluster_barrier();
+                // this CTA adds up its share of the rows and gives the result to all
+                const int r0 = kBlock * static_cast<int>(cta) / static_cast<int>(ctas),
+                          r1 = kBlock * (static_cast<int>(cta) + 1) / static_cast<int>(ctas);
+                // kItems places at once from each of at most kMost CTAs: 16 loads in flight
+                auto add_up = [&](auto items, auto most) {
+                    constexpr int kItems = decltype(items)::value, kMost = decltype(most)::value;
+                    const int total = (r1 - r0) * 32;
+                    for (int i0 = tid; i0 < total; i0 += kSmallThreads * kItems) {
+                        float4 q[kItems][kMost];
+#pragma unroll
+                        for (int j = 0; j < kItems; ++j) {
+                            const int i = i0 + j * kSmallThreads, r = r0 + i / 32, c = i % 32;
+                            if (i >= total) continue;
+                            const float4* from = reinterpret_cast<const float4*>(other) + r * 32 + (c ^ (r & 31));
+#pragma unroll
+                            for (int k = 0; k < kMost; ++k)
+                                if (k < static_cast<int>(ctas))
+                                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                                 : "=f"(q[j][k].x), "=f"(q[j][k].y), "=f"(q[j][k].z), "=f"(q[j][k].w)
+                                                 : "r"(remote_addr(from, k)));
+                        }
+#pragma unroll
+                        for (int j = 0; j < kItems; ++j) {
+                            const int i = i0 + j * kSmallThreads, r = r0 + i / 32, c = i % 32;
+                            if (i >= total) continue;
+                            float4 t = q[j][0];
+#pragma unroll
+                            for (int k = 1; k < kMost; ++k) {
+                                if (k >= static_cast<int>(ctas)) continue;
+                                t.x = __fadd_rn(t.x, q[j][k].x), t.y = __fadd_rn(t.y, q[j][k].y);
+                                t.z = __fadd_rn(t.z, q[j][k].z), t.w = __fadd_rn(t.w, q[j][k].w);
+                            }
+                            const __half2 h0 = __floats2half2_rn(__fmul_rn(t.x, gram_scale), __fmul_rn(t.y, gram_scale));
+                            const __half2 h1 = __floats2half2_rn(__fmul_rn(t.z, gram_scale), __fmul_rn(t.w, gram_scale));
+                            const unsigned char* to =
+                                a_op + c / 16 * kBlockBytes + swizzled(r, c % 16 / 2) + c % 2 * 8;
+                            for (uint32_t k = 0; k < ctas; ++k)
+                                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};"
+                                             ::"r"(remote_addr(to, k)), "r"(*reinterpret_cast<const uint32_t*>(&h0)),
+                                               "r"(*reinterpret_cast<const uint32_t*>(&h1)) : "memory");
+                        }
+                    }
+                };
+                if (ctas <= 4) add_up(Count<4>(), Count<4>());
+                else add_up(Count<1>(), Count<kSmallClusters>());
+            }
+        }
+        publish();
+        // B = b A + c A A, in A's place (the product has read A)
+        product([&] {
+            constexpr uint32_t idesc = kInstr | (static_cast<uint32_t>(kGramCols / 8) << 17);
+            for (int k = 0; k < k_a; k += 16) {
+                const uint64_t d = operand_desc(a_op + k / 64 * kBlockBytes, 16) + k % 64 / 16 * 2;
+                mma_f16<kPair>(s_tmem, d, d, idesc, k > 0);
+            }
+        });
+        {
+            float v[kGramCols / 2];
+#pragma unroll
+            for (int c = 0; c < kGramCols / 2; c += 32)
+                tmem_load_32(lanes + half * (kGramCols / 2) + c, reinterpret_cast<uint32_t*>(v) + c);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            const float f = __fmul_rn(s.c, 1.0f / kGramScale);
+            uint4 old[kGramCols / 16];
+#pragma unroll
+            for (int c = 0; c < kGramCols / 2; c += 8) {
+                const int col = half * (kGramCols / 2) + c;
+                old[c / 8] = *reinterpret_cast<const uint4*>(a_op + col / 64 * kBlockBytes + swizzled(row, col % 64 / 8));
+            }
+#pragma unroll
+            for (int c = 0; c < kGramCols / 2; c += 8) {
+                float y[8];
+                unpack_half8(old[c / 8], y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[c + i] = __fmaf_rn(s.b, y[i], __fmul_rn(f, v[c + i]));
+                const int col = half * (kGramCols / 2) + c;
+                *reinterpret_cast<uint4*>(a_op + col / 64 * kBlockBytes + swizzled(row, col % 64 / 8)) = pack_half8(v + c);
+            }
+        }
+        publish();
+        // X = a X + B X
+        product([&] {
+            const uint32_t n = kPair == 2 ? 256 : s.width;
+            const uint32_t idesc = kInstr | (1u << 16) | (n / 8 << 17);
+            for (int k = 0; k < k_a; k += 16) {
+                const uint64_t d = operand_desc(a_op + k / 64 * kBlockBytes, 16) + k % 64 / 16 * 2;
+                const unsigned char* x = kPair == 2 ? other + k / 128 * (2 * kBlockBytes) : x_op;
+                const uint64_t e = operand_desc(x + k % 128 * 128, kBlockBytes);
+                mma_f16<kPair>(s_tmem, d, e, idesc, k > 0);
+            }
+        });
+        const bool last = step + 1 == s.steps;
+        if (last) {   // no product reads shared memory any more: the result goes where it began
+            if (ctas > 1) cluster_barrier();
+            else __syncthreads();
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < kPerThread; c0 += 32) {
+            const int col = half * kPerThread + c0;
+            if (kPair == 1 && col >= s.width) break;
+            float v[32], x[32];
+            tmem_load_32(lanes + col, reinterpret_cast<uint32_t*>(v));
+            tmem_load_32(state + col, reinterpret_cast<uint32_t*>(x));
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __fmaf_rn(s.a, x[i], __fmul_rn(v[i], 1.0f / kGramScale));
+            if (last) {
+                const float f = __fdiv_rn(1.0f, p.x_scale);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) staging[row * kStagePitch + col + i] = __fmul_rn(x[i], f);
+            } else {
+                tmem_store_32(state + col, reinterpret_cast<const uint32_t*>(x));
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) put_x(col + i, pack_half8(x + i));
+            }
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        if (!last) publish();
+    }
+    __syncthreads();
+    const int across = s.tall ? kStagePitch : 1, down = s.tall ? 1 : kStagePitch;   // along and between lines
+    for (int line = warp; line < lines; line += kWarps) {
+        uint16_t* out = s.out + (b * p.rows + line0 + line) * p.cols + at0;
+        const float* from = staging + line * down;
+        if ((p.cols & 1) == 0) {   // pairs of values stay on 4 bytes
+            for (int at = 2 * lane; at < length; at += 64) {
+                if (!SPL_CHECK(at < length, kSiteOrthOut, at)) continue;
+                const float lo = from[at * across], hi = from[(at + 1) * across];
+                uint32_t w;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+                *reinterpret_cast<uint32_t*>(out + at) = w;
+            }
+        } else {
+            for (int at = lane; at < length; at += 32)
+                if (SPL_CHECK(at < length, kSiteOrthOut, at)) Vec16<true>::store1(out, at, from[at * across]);
+        }
+    }
+    if (late && tid == 0 && s.flags != nullptr) atomicOr(s.flags, kFlagTimeout);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    if (ctas > 1) cluster_barrier();
+    else __syncthreads();
+    if (warp == 0) {
+        if constexpr (kPair == 2)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "n"(512));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "n"(512));
+    }
+}
+
+// Whether a stack takes the small kernel: its matrices fit a cluster, and the clusters run in a few
+// waves.  Against the phases above: 64 x 64 22 and 67 us, 128 x 4096 65 and 141 us, 256 x 256 56 and
+// 91 us, 16 of 128 x 4096 192 and 292 us, but 64 of them (1,024 CTAs) 675 and 582 us.
+bool is_small(int64_t batch, int64_t m, int64_t n, int sms) {
+    if (m <= 2 * kBlock && n <= kSmallCols) return true;
+    const int64_t ctas = (n + kSmallCols - 1) / kSmallCols;
+    return m <= kBlock && ctas <= kSmallClusters && batch * ctas <= 4 * static_cast<int64_t>(sms);
+}
+
+template <int kPair, bool kBf16, bool kVec>
+cudaError_t launch_small(const SmallArgs& s, int64_t batch, cudaStream_t stream) {
+    const void* kern = reinterpret_cast<const void*>(&k_orth_small<kPair, kBf16, kVec>);
+    const int ctas = kPair == 2 ? 2 : (s.n + s.width - 1) / s.width;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallShape<kPair>::kSmem);
+    if (e == cudaSuccess && ctas > 8)   // beyond the portable cluster size
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(batch * ctas));
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = SmallShape<kPair>::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_orth_small<kPair, kBf16, kVec>, s);
+}
+
+}  // namespace
+}  // namespace spl
