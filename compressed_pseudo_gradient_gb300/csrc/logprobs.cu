@@ -33,7 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxParts = 16;
-constexpr int kMaxSegs = 36;             // segments per thread whose maxima are kept
+constexpr int kMaxSegs = 34;             // segments per thread whose maxima are kept
 constexpr int kMaxFound = kWarps * 64;   // segments, and candidates, that are listed
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kSafe = 1e30f;      // log2-domain magnitudes below this cannot overflow in a sum
@@ -100,25 +100,34 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 }
 
 // ---- sorted lists of the largest ------------------------------------------------------------
-__device__ __forceinline__ uint64_t rank_key(float x, uint32_t index) {
+// A value's bits in an order that unsigned numbers have; every NaN above all.
+__device__ __forceinline__ uint32_t value_order(float x) {
     const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));   // -0 ranks with +0
-    const uint32_t hi = x != x ? 0xffffffffu : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    return (static_cast<uint64_t>(hi) << 32) | (0xffffffffu - index);
+    return x != x ? 0xffffffffu : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float order_value(uint32_t o) {
+    return (o & 0x80000000u) ? (o == 0xffffffffu ? nan_f() : __uint_as_float(o & 0x7fffffffu))
+                             : __uint_as_float(~o);
+}
+
+__device__ __forceinline__ uint64_t rank_key(float x, uint32_t index) {
+    return (static_cast<uint64_t>(value_order(x)) << 32) | (0xffffffffu - index);
 }
 
 __device__ __forceinline__ float key_value(uint64_t key) {
-    const uint32_t hi = static_cast<uint32_t>(key >> 32);
-    return (hi & 0x80000000u) ? (hi == 0xffffffffu ? nan_f() : __uint_as_float(hi & 0x7fffffffu))
-                              : __uint_as_float(~hi);
+    return order_value(static_cast<uint32_t>(key >> 32));
 }
 
-__device__ __forceinline__ uint64_t order_pair(uint64_t k, int off, bool larger) {
-    const uint64_t o = __shfl_xor_sync(kAll, k, off);
+template <typename K>
+__device__ __forceinline__ K order_pair(K k, int off, bool larger) {
+    const K o = __shfl_xor_sync(kAll, k, off);
     return larger == (k > o) ? k : o;
 }
 
 // Descending over the lanes (bitonic).
-__device__ __forceinline__ uint64_t sort_descending(uint64_t k, int lane) {
+template <typename K>
+__device__ __forceinline__ K sort_descending(K k, int lane) {
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
@@ -129,9 +138,10 @@ __device__ __forceinline__ uint64_t sort_descending(uint64_t k, int lane) {
 
 // The 32 largest of two descending lists, descending: the larger of each entry and its mirror
 // is a bitonic sequence of the 32 largest, sorted by five exchanges.
-__device__ __forceinline__ uint64_t top_merge(uint64_t a, uint64_t b, int lane) {
-    const uint64_t r = __shfl_sync(kAll, b, 31 - lane);
-    uint64_t k = a > r ? a : r;
+template <typename K>
+__device__ __forceinline__ K top_merge(K a, K b, int lane) {
+    const K r = __shfl_sync(kAll, b, 31 - lane);
+    K k = a > r ? a : r;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) k = order_pair(k, off, (lane & off) == 0);
     return k;
@@ -145,7 +155,8 @@ struct TopList {
 };
 
 // The warps' lists into the first one's, in a fixed tree.
-__device__ __forceinline__ void merge_warps(uint64_t (*lists)[32], int warp, int lane) {
+template <typename K>
+__device__ __forceinline__ void merge_warps(K (*lists)[32], int warp, int lane) {
     for (int half = kWarps / 2; half > 0; half >>= 1) {
         if (warp < half) lists[warp][lane] = top_merge(lists[warp][lane], lists[warp + half][lane], lane);
         __syncthreads();
@@ -263,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const __grid_constant_
     constexpr int kN = V::kN;
     __shared__ Stats s_stats[kWarps];
     __shared__ uint64_t s_top[kTop ? kWarps : 1][32];
+    __shared__ uint32_t s_max[kTop ? kWarps : 1][32];
     __shared__ uint64_t s_found[kTop ? kMaxFound : 1];
     __shared__ float s_seg[kTop ? kMaxSegs : 1][kTop ? kThreads : 1];
     __shared__ uint32_t s_list[kTop ? kMaxFound : 1];
@@ -371,16 +383,17 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const __grid_constant_
     }
     if (tail > 0) scalars(done, tail);
 
+    bool several = false;   // lists, one per warp
     if constexpr (kTop) {
         if (in_seg > 0) {
             s_seg[seg++][tid] = seg_max;
             lane_max = max_nan(lane_max, seg_max);
         }
         if (tid == 0) s_segs_found = s_found_total = 0;
-        s_top[warp][lane] = sort_descending(rank_key(lane_max, tid), lane);
+        s_max[warp][lane] = sort_descending(value_order(lane_max), lane);
         __syncthreads();
-        merge_warps(s_top, warp, lane);
-        const float bound = key_value(s_top[0][a.top - 1]);
+        merge_warps(s_max, warp, lane);
+        const float bound = order_value(s_max[0][a.top - 1]);
         for (int q = 0; q < seg; ++q) {
             if (s_seg[q][tid] < bound) continue;
             const uint32_t at = atomicAdd(&s_segs_found, 1u);
@@ -446,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const __grid_constant_
                            static_cast<uint32_t>(done + lane), lane, a.top);
             top_flush(top, found, count, lane, a.top);
         }
-        __syncthreads();   // every thread has read the bound
-        s_top[warp][lane] = top.key;
+        if (full || warp == 0) s_top[warp][lane] = top.key;
+        several = full;
     }
 
     // join: lanes (one reference), the CTA's warps
@@ -459,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const __grid_constant_
     }
     if (lane == 0) s_stats[warp] = st;
     __syncthreads();
-    if constexpr (kTop) merge_warps(s_top, warp, lane);
+    if (kTop && several) merge_warps(s_top, warp, lane);
     const Stats none = {kLowest, 0.0f, 0.0f};
     if (warp == 0) st = join_warp(lane < kWarps ? s_stats[lane] : none, c);
     if (parts > 1) {   // the cluster's CTAs, in the first one
