@@ -13,6 +13,12 @@
 //     X that the other one's columns need.
 // X by rows serves the Gram product (rows along K) and, the same bytes read the other way, B X
 // (rows along N).
+//
+// With few rows the operands' roundings average out less (2.8e-3 of error at 40 rows, 1.9e-3 at
+// 100, against 1.7e-3 at 256), so for kPair = 1 the update also multiplies what they cut off, as
+// fp16 planes of its own (subnormals and all): B X is B_hi X_hi + B_lo X_hi, up to kFineRows rows
+// also + B_hi X_lo.  That leaves 1.3e-3 and 1.5e-3 and costs up to 1 us a step; X_lo for 128 rows
+// would cost another.
 #pragma once
 
 #include "orth_run.cuh"
@@ -23,6 +29,7 @@ namespace {
 constexpr int kSmallThreads = 256;
 constexpr int kSmallCols = 256;                    // of X per CTA
 constexpr int kSmallClusters = 16;
+constexpr int kFineRows = 64;
 constexpr int kStagePitch = kSmallCols + 1;        // floats; odd, so rows and columns both read freely
 constexpr int kBlockBytes = kBlock * kTileK * 2;   // 64 columns of an operand
 
@@ -30,10 +37,12 @@ template <int kPair>
 struct SmallShape {
     static constexpr int kGramCols = kBlock * kPair;
     static constexpr int kXBytes = kSmallCols / 64 * kBlockBytes;
+    static constexpr int kXLoBytes = kPair == 1 ? kXBytes : 0;
     static constexpr int kABytes = kGramCols / 64 * kBlockBytes;
-    // partial sums (kPair = 1), or the columns' half of X in all rows (kPair = 2)
+    // partial sums, and once they are added up the low plane of B (kPair = 1); or the columns' half
+    // of X in all rows (kPair = 2)
     static constexpr int kOtherBytes = kPair == 1 ? kBlock * kBlock * 4 : 2 * 2 * kBlockBytes;
-    static constexpr int kUsed = kXBytes + kABytes + kOtherBytes;
+    static constexpr int kUsed = kXBytes + kXLoBytes + kABytes + kOtherBytes;
     static constexpr int kStaging = kBlock * kStagePitch * 4;
     static constexpr int kSmem = (kUsed > kStaging ? kUsed : kStaging) + 1024;
 };
@@ -81,8 +90,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
     extern __shared__ unsigned char smem_raw[];
     unsigned char* x_op = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    unsigned char* a_op = x_op + S::kXBytes;
+    unsigned char* x_lo = x_op + S::kXBytes;
+    unsigned char* a_op = x_lo + S::kXLoBytes;
     unsigned char* other = a_op + S::kABytes;
+    unsigned char* b_lo = other;
     float* staging = reinterpret_cast<float*>(x_op);   // before the operands exist, and after
     __shared__ __align__(8) uint64_t bar;
     __shared__ uint32_t s_tmem;
@@ -175,9 +186,22 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
     const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = s_tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t state = lanes + kSmallCols;   // X in columns 256 .. 511, accumulators in 0 .. 255
+    const bool fine = kPair == 1 && s.m <= kFineRows;
+    // what 8 values lose in fp16
+    auto cut_off = [](const float* x, const uint4& hi) {
+        float y[8];
+        unpack_half8(hi, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __fsub_rn(x[i], y[i]);
+        return pack_half8(y);
+    };
     // 8 columns of the operand X from column c, and in a pair their copy with the columns' owner
-    auto put_x = [&](int c, const uint4& w) {
-        *reinterpret_cast<uint4*>(x_op + c / 64 * kBlockBytes + swizzled(row, c % 64 / 8)) = w;
+    auto put_x = [&](int c, const float* x) {
+        const uint4 w = pack_half8(x);
+        const int at = c / 64 * kBlockBytes + swizzled(row, c % 64 / 8);
+        *reinterpret_cast<uint4*>(x_op + at) = w;
+        if constexpr (kPair == 1)
+            if (fine) *reinterpret_cast<uint4*>(x_lo + at) = cut_off(x, w);
         if constexpr (kPair == 2) {
             const uint32_t to = remote_addr(other, c / 128) + cta * (2 * kBlockBytes) + c % 128 / 64 * kBlockBytes +
                                 swizzled(row, c % 64 / 8);
@@ -218,7 +242,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
         if (ctas > 1) cluster_barrier();   // a pair writes to the other's memory below
         else __syncthreads();
 #pragma unroll
-        for (int c = 0; c < kPerThread; c += 8) put_x(half * kPerThread + c, pack_half8(x + c));
+        for (int c = 0; c < kPerThread; c += 8) put_x(half * kPerThread + c, x + c);
 #pragma unroll
         for (int c = 0; c < kPerThread; c += 32)
             tmem_store_32(state + half * kPerThread + c, reinterpret_cast<const uint32_t*>(x) + c);
@@ -334,7 +358,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[c + i] = __fmaf_rn(s.b, y[i], __fmul_rn(f, v[c + i]));
                 const int col = half * (kGramCols / 2) + c;
-                *reinterpret_cast<uint4*>(a_op + col / 64 * kBlockBytes + swizzled(row, col % 64 / 8)) = pack_half8(v + c);
+                const int at = col / 64 * kBlockBytes + swizzled(row, col % 64 / 8);
+                const uint4 w = pack_half8(v + c);
+                *reinterpret_cast<uint4*>(a_op + at) = w;
+                if constexpr (kPair == 1) *reinterpret_cast<uint4*>(b_lo + at) = cut_off(v + c, w);
             }
         }
         publish();
@@ -347,6 +374,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
                 const unsigned char* x = kPair == 2 ? other + k / 128 * (2 * kBlockBytes) : x_op;
                 const uint64_t e = operand_desc(x + k % 128 * 128, kBlockBytes);
                 mma_f16<kPair>(s_tmem, d, e, idesc, k > 0);
+                if constexpr (kPair == 1) {
+                    const uint64_t dl = operand_desc(b_lo + k / 64 * kBlockBytes, 16) + k % 64 / 16 * 2;
+                    const uint64_t el = operand_desc(x_lo + k % 128 * 128, kBlockBytes);
+                    mma_f16<kPair>(s_tmem, dl, e, idesc, true);
+                    if (fine) mma_f16<kPair>(s_tmem, d, el, idesc, true);
+                }
             }
         });
         const bool last = step + 1 == s.steps;
@@ -371,7 +404,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
             } else {
                 tmem_store_32(state + col, reinterpret_cast<const uint32_t*>(x));
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) put_x(col + i, pack_half8(x + i));
+                for (int i = 0; i < 32; i += 8) put_x(col + i, x + i);
             }
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
