@@ -4,7 +4,7 @@
 //   out[t]     = scale table[id_t]
 //   d_table[v] = scale (sum of d_out[t] over the tokens t with id_t = v, in ascending t)
 //
-// The gradient first sorts the tokens by id (up to kSmallSort of them in one CTA's shared memory,
+// The gradient first sorts the tokens by id (up to kRankTokens of them by counting ranks,
 // more by a stable radix sort: digit counts per tile, a scan, a ranked scatter), then sums over
 // windows of consecutive sorted tokens: a run of
 // equal ids inside one window is summed and written at once, a run that crosses window borders
