@@ -211,12 +211,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
     };
     // what threads of the cluster wrote to shared memory, before the products read it
     auto publish = [&] {
-        fence_async_all();
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        if (ctas > 1) cluster_barrier();
-        else __syncthreads();
+        if (ctas > 1) {
+            asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+            cluster_barrier();
+        } else {
+            fence_async_smem();
+            __syncthreads();
+        }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        fence_async_all();
     };
     uint32_t bar_phase = 0;
     // one product: `issue` runs in the thread that issues it; then all wait for it
