@@ -135,6 +135,16 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
                      ::"r"(smem_addr(bar)) : "memory");
 }
 
+// One lane of a converged warp.  The roles that issue operand copies and MMAs run with their whole
+// warp and issue from the elected lane, so that the compiler knows the loops to be uniform: a pair's
+// 256 x 128 tile takes 0.25 us for a block of 64 along K, with a lone thread's loop 0.32 us (1024 x
+// 8192: 250 us against 268, 8192 x 8192 x 28672: 16.5 ms against 16.9).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Address of a shared variable in the pair's first CTA.
 __device__ __forceinline__ uint32_t leader_addr(const void* p) {
     uint32_t a;
@@ -431,113 +441,121 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
     const uint32_t tmem = s_tmem;
     bool late = false;
 
-    if (warp == 8) {
-        if (lane == 0) {   // operands
-            Dependencies<kPair> deps;
-            int stage = 0, used = 0;
-            uint32_t phase = 0;
-            for (int ph = 0; ph < run.num_phases && !late; ++ph) {
-                const Phase p = run.phases[ph];
-                if (p.reduce) continue;
-                const int units = T::units(run.m, run.batch, p);
-                for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
-                    const UnitAt at = T::at(run.m, p, u);
-                    if (!deps.wait(run, p, ph, at.b)) {
+    if (warp == 8) {   // operands
+        Dependencies<kPair> deps;
+        const bool issuer = elect_one();
+        const uint32_t full0 = kPair == 2 ? leader_addr(&full[0]) : smem_addr(&full[0]);
+        int stage = 0, used = 0;
+        uint32_t phase = 0;
+        for (int ph = 0; ph < run.num_phases && !late; ++ph) {
+            const Phase p = run.phases[ph];
+            if (p.reduce) continue;
+            const int cols = p.tile_n / kPair;   // of B per CTA: 128 or 64
+            const uint32_t bytes = kPair * (kOperandBytes + cols * kTileK * 2);
+            const CUtensorMap* map_a = &run.wide[p.a];
+            const CUtensorMap* map_b = p.b_along_n || cols == 64 ? &run.narrow[p.b] : &run.wide[p.b];
+            const int units = T::units(run.m, run.batch, p);
+            for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
+                const UnitAt at = T::at(run.m, p, u);
+                if (!__all_sync(kAll, deps.wait(run, p, ph, at.b))) {
+                    late = true;
+                    break;
+                }
+                const int row = at.i * T::kTile + rank * kBlock, col = at.j * p.tile_n + rank * cols;
+                for (int kb = at.k0; kb < at.k1; ++kb) {
+                    if (!__all_sync(kAll, mbar_wait(&empty[stage], phase ^ 1u))) {
                         late = true;
                         break;
                     }
-                    for (int kb = at.k0; kb < at.k1; ++kb) {
-                        if (!mbar_wait(&empty[stage], phase ^ 1u)) {
-                            late = true;
-                            break;
-                        }
-                        unsigned char* a = stages + stage * kStageBytes;
-                        unsigned char* b = a + kOperandBytes;
-                        const uint32_t bar = kPair == 2 ? leader_addr(&full[stage]) : smem_addr(&full[stage]);
-                        const int cols = p.tile_n / kPair;   // of B per CTA: 128 or 64
-                        if (rank == 0) mbar_expect_tx(&full[stage], kPair * (kOperandBytes + cols * kTileK * 2));
-                        const int row = at.i * T::kTile + rank * kBlock, col = at.j * p.tile_n + rank * cols;
-                        tma_load<kPair>(a, &run.wide[p.a], kb * kTileK, row, at.b, bar);
+                    unsigned char* a = stages + stage * kStageBytes;
+                    unsigned char* b = a + kOperandBytes;
+                    const uint32_t bar = full0 + stage * 8;
+                    if (issuer) {
+                        if (rank == 0) mbar_expect_tx(&full[stage], bytes);
+                        tma_load<kPair>(a, map_a, kb * kTileK, row, at.b, bar);
                         if (p.b_along_n) {
-                            tma_load<kPair>(b, &run.narrow[p.b], col, kb * kTileK, at.b, bar);
+                            tma_load<kPair>(b, map_b, col, kb * kTileK, at.b, bar);
                             if (cols > 64)
-                                tma_load<kPair>(b + kOperandBytes / 2, &run.narrow[p.b], col + 64, kb * kTileK, at.b,
-                                                bar);
+                                tma_load<kPair>(b + kOperandBytes / 2, map_b, col + 64, kb * kTileK, at.b, bar);
                         } else {
-                            tma_load<kPair>(b, cols > 64 ? &run.wide[p.b] : &run.narrow[p.b], kb * kTileK, col, at.b,
-                                            bar);
+                            tma_load<kPair>(b, map_b, kb * kTileK, col, at.b, bar);
                         }
-                        if (used < kStages) ++used;
-                        if (++stage == kStages) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                    }
+                    __syncwarp();
+                    if (used < kStages) ++used;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
             }
-            if (late) {
-                // the copies still in flight must land before the CTA leaves; a pair's are all
-                // counted in its first CTA, and the second waits for that one before it exits
-                bool pending = false;
-                for (int q = 0; q < used && rank == 0; ++q) {
-                    const int s = (stage + kStages - 1 - q) % kStages;
-                    pending |= !mbar_wait(&full[s], s < stage ? phase : phase ^ 1u);
-                }
-                if (run.flags != nullptr)
-                    atomicOr(run.flags, kFlagTimeout | (pending ? kFlagCopyPending : 0u));
+        }
+        if (late && lane == 0) {
+            // the copies still in flight must land before the CTA leaves; a pair's are all
+            // counted in its first CTA, and the second waits for that one before it exits
+            bool pending = false;
+            for (int q = 0; q < used && rank == 0; ++q) {
+                const int s = (stage + kStages - 1 - q) % kStages;
+                pending |= !mbar_wait(&full[s], s < stage ? phase : phase ^ 1u);
             }
+            if (run.flags != nullptr)
+                atomicOr(run.flags, kFlagTimeout | (pending ? kFlagCopyPending : 0u));
         }
         __syncwarp();
-    } else if (warp == 9) {
-        if (lane == 0 && rank == 0) {   // products
-            int stage = 0, acc = 0;
-            uint32_t phase = 0, acc_phase = 0;
-            for (int ph = 0; ph < run.num_phases && !late; ++ph) {
-                const Phase p = run.phases[ph];
-                if (p.reduce) continue;
-                // fp32 accumulators, fp16 operands, B transposed where its rows run along N
-                const uint32_t idesc = (1u << 4) | ((p.b_along_n ? 1u : 0u) << 16) |
-                                       (static_cast<uint32_t>(p.tile_n / 8) << 17) |
-                                       (static_cast<uint32_t>(T::kTile / 16) << 24);
-                const uint32_t lead = p.b_along_n ? kOperandBytes / 2 : 16;
-                const uint32_t b_step = p.b_along_n ? 128 : 2;   // 16 of K: 16 rows, or 32 bytes
-                const int units = T::units(run.m, run.batch, p);
-                for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
-                    const UnitAt at = T::at(run.m, p, u);
-                    if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u)) {
+    } else if (warp == 9) {   // products
+        const bool issuer = elect_one();
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        for (int ph = 0; ph < run.num_phases && !late && rank == 0; ++ph) {
+            const Phase p = run.phases[ph];
+            if (p.reduce) continue;
+            // fp32 accumulators, fp16 operands, B transposed where its rows run along N
+            const uint32_t idesc = (1u << 4) | ((p.b_along_n ? 1u : 0u) << 16) |
+                                   (static_cast<uint32_t>(p.tile_n / 8) << 17) |
+                                   (static_cast<uint32_t>(T::kTile / 16) << 24);
+            const uint32_t b_step = p.b_along_n ? 128 : 2;   // 16 of K: 16 rows, or 32 bytes
+            const uint64_t desc_a = operand_desc(stages, 16);
+            const uint64_t desc_b = operand_desc(stages + kOperandBytes, p.b_along_n ? kOperandBytes / 2 : 16);
+            const int units = T::units(run.m, run.batch, p);
+            for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
+                const UnitAt at = T::at(run.m, p, u);
+                if (!__all_sync(kAll, mbar_wait(&acc_empty[acc], acc_phase ^ 1u))) {
+                    late = true;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t d = tmem + acc * kAccCols;
+                for (int kb = at.k0; kb < at.k1; ++kb) {
+                    if (!__all_sync(kAll, mbar_wait(&full[stage], phase))) {
                         late = true;
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    for (int kb = at.k0; kb < at.k1; ++kb) {
-                        if (!mbar_wait(&full[stage], phase)) {
-                            late = true;
-                            break;
-                        }
-                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const unsigned char* a = stages + stage * kStageBytes;
-                        const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperandBytes, lead);
+                    const uint64_t da = desc_a + stage * (kStageBytes >> 4), db = desc_b + stage * (kStageBytes >> 4);
+                    if (issuer) {
 #pragma unroll
                         for (int k = 0; k < kTileK / 16; ++k)
-                            mma_f16<kPair>(tmem + acc * kAccCols, da + k * 2, db + k * b_step, idesc,
-                                           kb > at.k0 || k > 0);
+                            mma_f16<kPair>(d, da + k * 2, db + k * b_step, idesc, kb > at.k0 || k > 0);
                         mma_commit<kPair>(&empty[stage]);
-                        if (++stage == kStages) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
                     }
-                    if (late) break;
-                    mma_commit<kPair>(&acc_full[acc]);
-                    acc ^= 1;
-                    if (acc == 0) acc_phase ^= 1u;
+                    __syncwarp();
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
+                if (late) break;
+                if (issuer) mma_commit<kPair>(&acc_full[acc]);
+                __syncwarp();
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
             }
-            if (late) {
-                mma_commit<kPair>(&drain);
-                mbar_wait(&drain, 0);
-                if (run.flags != nullptr) atomicOr(run.flags, kFlagTimeout);
-            }
+        }
+        if (late) {
+            if (issuer) mma_commit<kPair>(&drain);
+            __syncwarp();
+            mbar_wait(&drain, 0);
+            if (lane == 0 && run.flags != nullptr) atomicOr(run.flags, kFlagTimeout);
         }
         __syncwarp();
     } else if (warp == 10) {

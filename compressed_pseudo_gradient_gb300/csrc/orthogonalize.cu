@@ -211,10 +211,13 @@ struct PhaseList {
 // product with fewer tiles than groups and a long K is split along K where that pays, followed by
 // a phase that sums the parts.  Measured: a block of 64 along K takes 0.28 us for a 128 x 128 tile
 // alone on its SM (its 32 KB arrive from L2 no faster) and 0.44 us with all SMs at it (L2's own
-// limit), 0.32 us for a pair's 256 x 256 tile and 0.2 us for 256 x 128; an epilogue 1 us and 0.8 us
-// for each slab of 64 columns, two slabs at a time; and 5 us from a phase's last result to the
-// next one's first product.  A stack's phases flow into one another, so that they take either the
-// time of their work or one matrix's way through them.
+// limit), 0.29 to 0.36 us for a pair's 256 x 256 tile and 0.25 us for 256 x 128 (24 KB a CTA, again
+// what L2 delivers to an SM), entered here as 0.2, the plans of which measured better (with 0.25:
+// 1024 x 4096 218 us instead of 194, 512 x 16384 252 instead of 241, 21 other shapes the same); an
+// epilogue 1 us and 0.8 us for each slab of 64 columns, two slabs at a time; and 5 us from a phase's
+// last result to the next one's first product (3 us entered here: 768 x 2000 153 us instead of
+// 147).  A stack's phases flow into one another, so that they take either the time of their work or
+// one matrix's way through them.
 template <int kPair>
 double plan(const PhaseList& list, const OrthRun& run, int groups, size_t partial_bytes, OrthRun* out) {
     using T = Tiling<kPair>;
