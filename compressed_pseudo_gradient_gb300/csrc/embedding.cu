@@ -4,15 +4,14 @@
 //   out[t]     = scale table[id_t]
 //   d_table[v] = scale (sum of d_out[t] over the tokens t with id_t = v, in ascending t)
 //
-// The gradient first sorts the tokens by id (up to kRankTokens of them by counting ranks,
-// more by a stable radix sort: digit counts per tile, a scan, a ranked scatter), then sums over
-// windows of consecutive sorted tokens: a run of
-// equal ids inside one window is summed and written at once, a run that crosses window borders
-// leaves one partial sum per window, joined in window order afterwards.  The work per CTA is
-// thus the same however often an id repeats, no floating-point atomics are used, and every run
-// gives the same bits.  Rows without tokens are zeroed by CTAs of the summing launch, found in a
-// bitmap of the ids seen; beside a small sort, which leaves the GPU idle, the whole table is
-// zeroed instead.
+// The gradient first sorts the tokens by id (up to kRankTokens of them by counting ranks, more by
+// a stable radix sort: digit counts per tile, a scan, a ranked scatter), then sums over windows of
+// consecutive sorted tokens: a run of equal ids inside one window is summed and written at once, a
+// run that crosses window borders leaves one partial sum per window, joined in window order
+// afterwards.  The work per CTA is thus the same however often an id repeats, no floating-point
+// atomics are used, and every run gives the same bits.  Rows without tokens are zeroed by CTAs of
+// the summing launch, found in a bitmap of the ids seen; beside a small sort, which leaves the GPU
+// idle, the whole table is zeroed instead.
 #include "local_device.cuh"
 #include "local_kernels.h"
 
@@ -130,8 +129,8 @@ __device__ __forceinline__ void zero_table(const ZeroTable& z, int64_t cta, int6
 
 // Few tokens: a token's place is the number of tokens that sort before it, counted against all
 // keys in shared memory by kRankLanes threads.  No step waits for another CTA, but the work grows
-// with the square: the whole accumulating call takes 24 us for 4,096 tokens of width 1024 (37 us
-// with the radix sort below) and 45 us for 8,192 (42 us).
+// with the square: the whole accumulating call takes 21 us for 4,096 tokens of width 1024 (35 us
+// with the radix sort below) and 40 us for 8,192 (37 us).
 constexpr int kRankTokens = 4096;    // most tokens sorted this way
 constexpr int kRankThreads = 256;
 constexpr int kRankLanes = 8;
@@ -139,6 +138,7 @@ constexpr int kRankLanes = 8;
 __global__ void __launch_bounds__(kRankThreads)
 k_sort_rank(const __grid_constant__ SortArgs p, const __grid_constant__ ZeroTable z) {
     constexpr uint32_t kPerCta = kRankThreads / kRankLanes;
+    let_next_start();
     if (blockIdx.x >= p.tiles) {
         zero_table(z, blockIdx.x - p.tiles, gridDim.x - p.tiles);
         return;
@@ -197,6 +197,7 @@ __device__ __forceinline__ bool sort_barrier(const SortArgs& p, int step) {
 
 __global__ void __launch_bounds__(kSortThreads, 1)
 k_sort_radix(const __grid_constant__ SortArgs p, const __grid_constant__ ZeroTable z) {
+    let_next_start();
     if (blockIdx.x >= p.tiles) {
         zero_table(z, blockIdx.x - p.tiles, gridDim.x - p.tiles);
         return;
@@ -301,8 +302,9 @@ k_sort_radix(const __grid_constant__ SortArgs p, const __grid_constant__ ZeroTab
 
 // ---- sums -----------------------------------------------------------------------------------
 // Sorted tokens per window.  Short windows give small gradients enough CTAs (2,000 tokens of
-// width 1001: 32 us for the call with windows of 16, 45 us with 64); long ones leave fewer partial
-// sums (16,384 of width 4096: 161 against 132 us; 32,768 of width 512: 138 against 125 us).
+// width 1001: 28 us for the call with windows of 16, 37 us with 64; 8,192 of 1024: 40 and 58 us);
+// long ones leave fewer partial sums, which counts where ids repeat (half of 65,536 of width 512 the
+// same: 789 us with 16, 328 us with 64; every id about as often: 159 and 182 us).
 constexpr int kWindow = 64;
 constexpr int kShortWindow = 16;
 constexpr int64_t kShortWindowValues = int64_t{1} << 23;   // up to this many values of d_out
@@ -400,6 +402,8 @@ template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kThreads, 4)
 k_grad_windows(const __grid_constant__ GradSums g, uint32_t sum_ctas, uint32_t zero_rows) {
     using U = Unit<kBf16, kVec>;
+    let_next_start();
+    after_previous();
     if (blockIdx.x >= sum_ctas) {   // zero the rows without tokens
         const uint32_t row0 = (blockIdx.x - sum_ctas) * zero_rows;
         for (uint32_t r = row0; r < row0 + zero_rows && r < g.vocab; ++r) {
@@ -468,6 +472,7 @@ k_grad_windows(const __grid_constant__ GradSums g, uint32_t sum_ctas, uint32_t z
 template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kThreads) k_grad_join(const __grid_constant__ GradSums g) {
     using U = Unit<kBf16, kVec>;
+    after_previous();
     const uint32_t per_cta = kThreads / g.cols;
     const uint32_t win = blockIdx.x / g.col_blocks * per_cta + threadIdx.x / g.cols;
     const int64_t unit = static_cast<int64_t>(blockIdx.x % g.col_blocks) * g.cols + threadIdx.x % g.cols;
@@ -555,12 +560,12 @@ cudaError_t launch_sums(GradSums g, cudaStream_t stream) {
     if (zero_rows < 1) zero_rows = 1;
     const uint32_t zero_ctas = g.seen == nullptr ? 0 : (g.vocab + zero_rows - 1) / zero_rows;
     if (sum_ctas + zero_ctas > 0) {
-        k_grad_windows<kBf16, kVec><<<sum_ctas + zero_ctas, kThreads, 0, stream>>>(g, sum_ctas, zero_rows);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_behind(k_grad_windows<kBf16, kVec>, dim3(sum_ctas + zero_ctas), kThreads,
+                                            stream, g, sum_ctas, zero_rows);
         if (e != cudaSuccess) return e;
     }
-    if (g.windows > 1) k_grad_join<kBf16, kVec><<<sum_ctas, kThreads, 0, stream>>>(g);
-    return cudaGetLastError();
+    if (g.windows > 1) return launch_behind(k_grad_join<kBf16, kVec>, dim3(sum_ctas), kThreads, stream, g);
+    return cudaSuccess;
 }
 
 // Enqueues the sort, and beside it the zeroing of the table if z has rows.
@@ -639,8 +644,8 @@ cudaError_t launch_embedding_grad(const EmbeddingGradArgs& a, bool bf16, cudaStr
     if (e != cudaSuccess) return e;
     const bool zero = !a.accumulate, radix = a.count > kRankTokens;
     // Zeroing the whole table beside the sort writes the tokens' rows twice; with many tokens it
-    // is left to the summing kernel, which knows them from the bitmap (16,384 tokens of width 1024,
-    // 32,768 ids: 54 us beside the sort, 62 us after it; 32,768 tokens of width 2048: 145 and 136).
+    // is left to the summing kernel, which knows them from the bitmap (8,192 tokens of width 1024,
+    // 32,768 ids: 40 us beside the sort, 49 us after it; 32,768 tokens of width 2048: 125 and 116).
     const bool zero_all = zero && (!radix || a.count * a.width <= (int64_t{1} << 25));
     SortArgs p = {};
     p.ids = a.ids;

@@ -23,6 +23,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Between the kernels of one call (launch_behind): the next one may be made resident from here on,
+// and the previous one's results are there from here on.
+__device__ __forceinline__ void let_next_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // max(a, b), NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float y;

@@ -16,6 +16,26 @@ struct TokenIds {
 // The current device's SM count, asked for once per device.
 cudaError_t sm_count(int* sms);
 
+// Launches a kernel of a call behind the call's previous one: its CTAs may become resident while
+// that one ends, and wait for its results where they call after_previous().  Every thread of such
+// a kernel calls that before it returns, so that the kernel ends after all of the call before it.
+// Saves 1 to 2 us a launch (2,000 tokens' embedding gradient 30.9 us against 34.7 one call after the
+// other, accumulating 21 against 26; orthogonalize 300 x 1000 117 against 120).
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, unsigned threads, cudaStream_t stream,
+                          Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 constexpr int kMaxTop = 32;   // alternatives per row: one list entry per lane of a warp
 
 struct LogprobsArgs {

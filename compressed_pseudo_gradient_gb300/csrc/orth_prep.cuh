@@ -81,6 +81,7 @@ struct PrepUnit {
 // The momentum step and each CTA's share of |u|^2.
 template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kPrepThreads) k_orth_norm(const __grid_constant__ PrepArgs p) {
+    let_next_start();
     using U = PrepUnit<kBf16, kVec>;
     __shared__ double s_sum[kPrepThreads / 32];
     const int64_t b = blockIdx.y;
@@ -182,6 +183,8 @@ __device__ __forceinline__ void store_state(const PrepArgs& p, int64_t at, const
 // X = u / (|u| + eps) in the state's format.
 template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kPrepThreads) k_orth_state(const __grid_constant__ PrepArgs p) {
+    let_next_start();
+    after_previous();
     using U = PrepUnit<kBf16, kVec>;
     const int64_t b = blockIdx.y;
     const float f = state_factor(p, b);
@@ -218,6 +221,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_orth_state(const __grid_consta
 // The same for a tall matrix, whose state is its transpose: 64 x 64 tiles through shared memory.
 template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kPrepThreads) k_orth_state_tall(const __grid_constant__ PrepArgs p) {
+    let_next_start();
+    after_previous();
     using U = PrepUnit<kBf16, kVec>;
     constexpr int kAcross = 64 / U::kN, kDown = kPrepThreads / kAcross;
     __shared__ float s_tile[64][65];
@@ -261,16 +266,16 @@ cudaError_t launch_prep(PrepArgs p, int64_t batch, bool tall, int sms, cudaStrea
     p.num_partials = static_cast<int>(ctas < kMaxPartials ? ctas : kMaxPartials);
     const unsigned b = static_cast<unsigned>(batch);
     k_orth_norm<kBf16, kVec><<<dim3(static_cast<unsigned>(p.num_partials), b), kPrepThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     const int64_t most = 8 * static_cast<int64_t>(sms);   // as many as are resident, then loop
     if (tall) {
         const int64_t tiles = (p.rows + 63) / 64 * ((p.cols + 63) / 64);
-        k_orth_state_tall<kBf16, kVec><<<dim3(static_cast<unsigned>(tiles < most ? tiles : most), b), kPrepThreads,
-                                         0, stream>>>(p);
-    } else {
-        k_orth_state<kBf16, kVec><<<dim3(static_cast<unsigned>(ctas < most ? ctas : most), b), kPrepThreads, 0,
-                                    stream>>>(p);
+        return launch_behind(k_orth_state_tall<kBf16, kVec>,
+                             dim3(static_cast<unsigned>(tiles < most ? tiles : most), b), kPrepThreads, stream, p);
     }
-    return cudaGetLastError();
+    return launch_behind(k_orth_state<kBf16, kVec>, dim3(static_cast<unsigned>(ctas < most ? ctas : most), b),
+                         kPrepThreads, stream, p);
 }
 
 }  // namespace

@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
     bool late = false;
+    after_previous();
 
     if (warp == 8) {   // operands
         Dependencies<kPair> deps;
@@ -800,6 +801,7 @@ k_orth_finish(const __half* __restrict__ hi, const __half* __restrict__ lo, int6
               int64_t m, int64_t n, float f, uint16_t* __restrict__ out, bool tall) {
     __shared__ float s_tile[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    after_previous();
     const int64_t b = blockIdx.z, r0 = static_cast<int64_t>(blockIdx.y) * 32,
                   c0 = static_cast<int64_t>(blockIdx.x) * 32;
 #pragma unroll

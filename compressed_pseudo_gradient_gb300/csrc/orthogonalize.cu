@@ -314,15 +314,17 @@ cudaError_t launch_run(const OrthRun& run, int groups, cudaStream_t stream) {
     cfg.blockDim = dim3(kRunThreads);
     cfg.dynamicSmemBytes = kRunSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute at[2];
+    cudaLaunchAttribute at[3];
     at[0].id = cudaLaunchAttributeCooperative;
     at[0].val.cooperative = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = kPair;
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
+    at[2].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see launch_behind
+    at[2].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 3;
     return cudaLaunchKernelEx(&cfg, k_orth_run<kPair>, run);
 }
 
@@ -530,10 +532,9 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& a, bool bf16, cudaStre
     if (e != cudaSuccess || direct) return e;
     const dim3 grid(static_cast<unsigned>((l.n + 31) / 32), static_cast<unsigned>((l.m + 31) / 32),
                     static_cast<unsigned>(a.batch));
-    k_orth_finish<<<grid, 256, 0, stream>>>(reinterpret_cast<const __half*>(ws + l.hi[x]),
-                                            reinterpret_cast<const __half*>(ws + l.lo[x]), l.ldx,
-                                            l.m * l.ldx, l.m, l.n, 1.0f / p.x_scale, a.out, tall);
-    return cudaGetLastError();
+    return launch_behind(k_orth_finish, grid, 256, stream, reinterpret_cast<const __half*>(ws + l.hi[x]),
+                         reinterpret_cast<const __half*>(ws + l.lo[x]), l.ldx, l.m * l.ldx, l.m, l.n,
+                         1.0f / p.x_scale, a.out, tall);
 }
 
 }  // namespace spl
