@@ -301,15 +301,17 @@ k_sort_radix(const __grid_constant__ SortArgs p, const __grid_constant__ ZeroTab
 }
 
 // ---- sums -----------------------------------------------------------------------------------
-// Sorted tokens per window.  Short windows give small gradients enough CTAs (2,000 tokens of
-// width 1001: 28 us for the call with windows of 16, 37 us with 64; 8,192 of 1024: 40 and 58 us);
-// long ones leave fewer partial sums, which counts where ids repeat (half of 65,536 of width 512 the
-// same: 789 us with 16, 328 us with 64; every id about as often: 159 and 182 us).
-constexpr int kWindow = 64;
-constexpr int kShortWindow = 16;
-constexpr int64_t kShortWindowValues = int64_t{1} << 23;   // up to this many values of d_out
+// Sorted tokens per window.  Short windows give small gradients enough CTAs, long ones leave fewer
+// partial sums to large ones.  With 16, 32 and 64 tokens a window, ids of a power law: 2,000 of
+// width 1001 30, 32 and 38 us for the call; 16,384 of 512 40, 48 and 62; 32,768 of 1024 70, 69 and
+// 84; 65,536 of 2048, half of them the same id, 475, 429 and 408; 65,536 of 8192 1,404, 1,362 and
+// 1,353.
+constexpr int kMaxWindow = 64;
 
-int window_of(int64_t count, int64_t width) { return count * width <= kShortWindowValues ? kShortWindow : kWindow; }
+int window_of(int64_t count, int64_t width) {
+    const int64_t values = count * width;   // of d_out
+    return values <= int64_t{1} << 23 ? 16 : values <= int64_t{1} << 26 ? 32 : kMaxWindow;
+}
 
 struct GradSums {
     const uint32_t* keys;   // sorted ids
@@ -419,7 +421,7 @@ k_grad_windows(const __grid_constant__ GradSums g, uint32_t sum_ctas, uint32_t z
         return;
     }
     // windows of this CTA (per_cta of them, kThreads / cols), with one key past each end
-    constexpr int kMaxStaged = kThreads / 8 * kWindow + 2;
+    constexpr int kMaxStaged = kThreads / 8 * kMaxWindow + 2;
     __shared__ uint32_t s_key[kMaxStaged], s_pos[kMaxStaged];
     const uint32_t per_cta = kThreads / g.cols;
     const uint32_t win0 = blockIdx.x / g.col_blocks * per_cta;
@@ -467,16 +469,83 @@ k_grad_windows(const __grid_constant__ GradSums g, uint32_t sum_ctas, uint32_t z
     }
 }
 
-// Joins the partial sums of a run that crosses windows; the window it starts in owns it.  The
-// threads first find together, 32 windows at a time, how far the run reaches.
+// Adds the partial sums of windows first .. last - 1 of a run that came from the left.
+template <typename U>
+__device__ __forceinline__ void add_heads(const GradSums& g, U& sum, uint32_t first, uint32_t last, int64_t col) {
+    constexpr uint32_t kAhead = 16;   // loads in flight: their latency bounds a long run's sum
+    uint32_t w = first;
+    for (; w + kAhead <= last; w += kAhead) {
+        U v[kAhead];
+#pragma unroll
+        for (uint32_t j = 0; j < kAhead; ++j)
+            v[j].load_f32(g.partials + 2 * static_cast<int64_t>(w + j) * g.width + col);
+#pragma unroll
+        for (uint32_t j = 0; j < kAhead; ++j) sum.add(v[j]);
+    }
+    for (; w < last; ++w) {
+        U v;
+        v.load_f32(g.partials + 2 * static_cast<int64_t>(w) * g.width + col);
+        sum.add(v);
+    }
+}
+
+// Joins the partial sums of a run that crosses windows.  The first CTAs take the runs that reach
+// into a window whose number is a multiple of kAnchor, one CTA per such window and 32 units: its
+// warps sum a share of the run each, added in order afterwards, so that a common id is no chain of
+// hundreds of dependent loads (65,536 tokens of width 512, half of them the same: 184 us, as one
+// chain 304 us; 65,536 of width 64 by a power law: 45 and 98 us).  The others take the rest, at most
+// kAnchor windows long, a thread per unit and window; the window a run starts in owns it.
+constexpr uint32_t kAnchor = 32;
+
 template <bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kThreads) k_grad_join(const __grid_constant__ GradSums g) {
+__global__ void __launch_bounds__(kThreads)
+k_grad_join(const __grid_constant__ GradSums g, uint32_t anchored, uint32_t anchored_blocks) {
     using U = Unit<kBf16, kVec>;
     after_previous();
-    const uint32_t per_cta = kThreads / g.cols;
-    const uint32_t win = blockIdx.x / g.col_blocks * per_cta + threadIdx.x / g.cols;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x % g.col_blocks) * g.cols + threadIdx.x % g.cols;
     const uint32_t lane = threadIdx.x & 31;
+    if (blockIdx.x < anchored) {
+        constexpr int kShares = kThreads / 32;
+        __shared__ float s_sum[kShares][32 * U::kN];
+        const uint32_t a = (blockIdx.x / anchored_blocks + 1) * kAnchor, share = threadIdx.x / 32;
+        const uint32_t key = g.keys[a * g.window];
+        // whether the run enters window w from the left
+        auto enters = [&](uint32_t w) {
+            return w > 0 && g.keys[w * g.window] == key && g.keys[w * g.window - 1] == key;
+        };
+        if (key >= g.vocab || !enters(a)) return;
+        const unsigned before = __ballot_sync(kAll, enters(a - 1 - lane));
+        if (before == kAll) return;   // the multiple before this one has it
+        const uint32_t owner = a - __ffs(~before);
+        uint32_t last = a, reach = g.windows;   // keys are sorted: search between them
+        while (reach - last > 1) {
+            const uint32_t step = (reach - last + 31) / 32, w = last + (lane + 1) * step;
+            const bool in = w < reach && g.keys[w * g.window] == key;
+            last += __popc(__ballot_sync(kAll, in)) * step;
+            reach = min(reach, last + step);
+        }
+        const int64_t unit = static_cast<int64_t>(blockIdx.x % anchored_blocks) * 32 + lane, col = unit * U::kN;
+        const bool inside = col < g.width;
+        const uint32_t per = (reach - owner + kShares - 1) / kShares, from = owner + share * per;
+        U sum;
+        sum.zero();
+        if (inside) {
+            if (share == 0) sum.load_f32(g.partials + (2 * static_cast<int64_t>(owner) + 1) * g.width + col);
+            add_heads(g, sum, share == 0 ? owner + 1 : from, min(from + per, reach), col);
+        }
+#pragma unroll
+        for (int i = 0; i < U::kN; ++i) s_sum[share][i * 32 + lane] = sum.x[i];
+        __syncthreads();
+        if (share > 0 || !inside) return;
+        for (int q = 1; q < kShares; ++q)
+#pragma unroll
+            for (int i = 0; i < U::kN; ++i) sum.x[i] = __fadd_rn(sum.x[i], s_sum[q][i * 32 + lane]);
+        if (SPL_CHECK(key < g.vocab, kSiteRowsOut, key))
+            sum.finish(g.d_table + key * g.stride + col, g.scale, g.accumulate);
+        return;
+    }
+    const uint32_t per_cta = kThreads / g.cols, cta = blockIdx.x - anchored;
+    const uint32_t win = cta / g.col_blocks * per_cta + threadIdx.x / g.cols;
+    const int64_t unit = static_cast<int64_t>(cta % g.col_blocks) * g.cols + threadIdx.x % g.cols;
     bool owns = win + 1 < g.windows && unit * U::kN < g.width;
     uint32_t key = 0;
     if (owns) {
@@ -485,30 +554,24 @@ __global__ void __launch_bounds__(kThreads) k_grad_join(const __grid_constant__ 
         owns = key < g.vocab && g.keys[next] == key &&                      // a run leaves this window
                !(first > 0 && g.keys[first] == key && g.keys[first - 1] == key);   // and starts in it
     }
+    const uint32_t anchor = (win / kAnchor + 1) * kAnchor;
     uint32_t reach = win + 1;   // one past the run's last window
     if (g.cols >= 32) {   // a warp has one window
         if (!__any_sync(kAll, owns)) return;
         const uint32_t k = __reduce_max_sync(kAll, owns ? key : 0u);
-        for (uint32_t w = win + 1;; w += 32) {
-            const bool in = w + lane < g.windows && g.keys[(w + lane) * g.window] == k;
-            const unsigned run = __ballot_sync(kAll, in);
-            reach = w + (run == kAll ? 32 : __ffs(~run) - 1);
-            if (run != kAll) break;
-        }
+        const bool in = reach + lane < g.windows && g.keys[(reach + lane) * g.window] == k;
+        const unsigned run = __ballot_sync(kAll, in);
+        reach += run == kAll ? 32 : __ffs(~run) - 1;
         if (!owns) return;
     } else {
         if (!owns) return;
-        while (reach < g.windows && g.keys[reach * g.window] == key) ++reach;
+        while (reach <= anchor && reach < g.windows && g.keys[reach * g.window] == key) ++reach;
     }
+    if (reach > anchor) return;   // taken above
     const int64_t col = unit * U::kN;
     U sum;
     sum.load_f32(g.partials + (2 * static_cast<int64_t>(win) + 1) * g.width + col);
-#pragma unroll 4
-    for (uint32_t w = win + 1; w < reach; ++w) {
-        U v;
-        v.load_f32(g.partials + 2 * static_cast<int64_t>(w) * g.width + col);
-        sum.add(v);
-    }
+    add_heads(g, sum, win + 1, reach, col);
     if (SPL_CHECK(key < g.vocab, kSiteRowsOut, key))
         sum.finish(g.d_table + key * g.stride + col, g.scale, g.accumulate);
 }
@@ -564,8 +627,11 @@ cudaError_t launch_sums(GradSums g, cudaStream_t stream) {
                                             stream, g, sum_ctas, zero_rows);
         if (e != cudaSuccess) return e;
     }
-    if (g.windows > 1) return launch_behind(k_grad_join<kBf16, kVec>, dim3(sum_ctas), kThreads, stream, g);
-    return cudaSuccess;
+    if (g.windows <= 1) return cudaSuccess;
+    const uint32_t anchored_blocks = static_cast<uint32_t>((units + 31) / 32);
+    const uint32_t anchored = (g.windows - 1) / kAnchor * anchored_blocks;
+    return launch_behind(k_grad_join<kBf16, kVec>, dim3(anchored + sum_ctas), kThreads, stream, g, anchored,
+                         anchored_blocks);
 }
 
 // Enqueues the sort, and beside it the zeroing of the table if z has rows.

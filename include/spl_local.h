@@ -98,7 +98,7 @@ size_t spl_embedding_grad_workspace(size_t count, size_t vocab, size_t width);
  * accumulate 1: the sums are added to d_table, rows without tokens are left alone.
  * Tokens with ids[i] = padding_id take no part (-1: no such id).  Tokens outside the table take
  * no part either and set SPL_FLAG_BAD_TOKEN.  Tokens of one id are added in ascending i within
- * groups of at most 64, groups in order.
+ * groups of at most 64; the groups' sums in order, those of an id with many in up to 8 shares first.
  *
  * d_out: [count][width] of `dtype`, d_out_stride >= width;  d_table: [vocab][width] fp32,
  * table_stride >= width.  count, vocab and width are below 2^31.

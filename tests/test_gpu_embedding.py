@@ -88,6 +88,31 @@ def test_grad_sums(count, vocab, width, dtype):
     assert torch.equal(acc[untouched], base[untouched])
 
 
+@pytest.mark.parametrize("width,lengths", [
+    # sums are split every 16 tokens and again every 512 (every 32 and 1,024, 64 and 2,048 for the
+    # last two): runs that end and begin there, beside it, and reach over many of them
+    (33, [512, 512, 1, 511, 16, 496, 1024, 15, 497, 513, 3, 4096, 17]),
+    (64, [4097, 15, 16, 1, 30000, 2, 510, 512, 1]),
+    (520, [511, 1537, 16, 2048, 1, 1, 512 * 7 - 2, 600]),
+    (1000, [1, 1023, 1024, 2047, 32, 33, 4096, 31, 20000]),
+    (1000, [2048, 2047, 1, 1, 4095, 64, 65, 63, 40000, 4096, 20000])])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_grad_of_long_runs(width, lengths, dtype):
+    g = gen(width + len(lengths))
+    vocab = len(lengths) + 1
+    ids = torch.arange(vocab - 1, device=DEV).repeat_interleave(torch.tensor(lengths, device=DEV))
+    ids = ids[torch.randperm(ids.numel(), generator=g, device=DEV)]
+    d_out = torch.randn(ids.numel(), width, generator=g, device=DEV).to(dtype)
+    ref, tol = reference(ids, d_out, vocab, 0.7)
+    got = spl.embedding_grad(ids, d_out, vocab, scale=0.7)
+    assert ((got.double() - ref).abs() <= tol).all()
+    assert torch.equal(spl.embedding_grad(ids, d_out, vocab, scale=0.7), got)
+    base = torch.randn(vocab, width, generator=g, device=DEV)
+    acc = base.clone()
+    spl.embedding_grad(ids, d_out, vocab, scale=0.7, out=acc, accumulate=True)
+    assert ((acc.double() - (base.double() + ref)).abs() <= tol + 2.0 ** -23 * (base.abs() + ref.abs())).all()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_grad_strides_padding_and_bad_ids(dtype):
     g = gen(1)
