@@ -443,13 +443,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_orth_small(const __grid_co
     }
 }
 
-// Whether a stack takes the small kernel: its matrices fit a cluster, and the clusters run in a few
-// waves.  Against the phases above: 64 x 64 22 and 67 us, 128 x 4096 65 and 141 us, 256 x 256 56 and
-// 91 us, 16 of 128 x 4096 192 and 292 us, but 64 of them (1,024 CTAs) 675 and 582 us.
+// Whether a stack takes the small kernel: its matrices fit a cluster, and clusters of more than 4 CTAs,
+// of which few fit beside each other, run in a few waves.  Against the phases above: 64 x 64 24 and
+// 60 us, 128 x 4096 69 and 125 us, 256 x 256 55 and 76 us; 600 of 128 x 512 487 and 692 us, 600 of
+// 128 x 1024 1,045 and 1,158 us; 28 of 128 x 4096 (448 CTAs) 282 and 310 us, but 32 of them 361 and
+// 322 us, and 76 of 128 x 2048 395 and 356 us.
 bool is_small(int64_t batch, int64_t m, int64_t n, int sms) {
     if (m <= 2 * kBlock && n <= kSmallCols) return true;
     const int64_t ctas = (n + kSmallCols - 1) / kSmallCols;
-    return m <= kBlock && ctas <= kSmallClusters && batch * ctas <= 4 * static_cast<int64_t>(sms);
+    return m <= kBlock && ctas <= kSmallClusters && (ctas <= 4 || batch * ctas <= 3 * static_cast<int64_t>(sms));
 }
 
 template <int kPair, bool kBf16, bool kVec>
