@@ -12,7 +12,6 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kGramScale = 1024.0f;    // of A and B
-constexpr float kLoScale = 2048.0f;      // of the state's low plane
 
 constexpr int kPrepThreads = 256;
 constexpr int kMaxPartials = 1216;  // sums of squares per matrix: eight CTAs per SM
@@ -159,7 +158,7 @@ __device__ __forceinline__ float nan_value() { return __uint_as_float(0x7fc00000
 
 __device__ __forceinline__ void split_state(float x, __half& hi, __half& lo) {
     hi = __float2half_rn(x);
-    lo = __float2half_rn(__fmul_rn(__fsub_rn(x, __half2float(hi)), kLoScale));
+    lo = __float2half_rn(__fsub_rn(x, __half2float(hi)));
 }
 
 // kN consecutive values of the state's two planes.

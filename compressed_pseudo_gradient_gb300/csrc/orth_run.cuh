@@ -58,6 +58,8 @@ enum ResultKind : uint8_t { kPlane, kState, kBf16, kBf16Transposed, kPartial };
 
 struct Phase {
     uint8_t a, b, src1, src2, dst, dst_lo;   // matrices, or kNone
+    uint8_t a_lo, b_lo;                      // operands' low planes
+    uint8_t terms;                           // 1: a b;  3: a b + a_lo b + a b_lo, one K after the other
     uint8_t result;                          // ResultKind
     bool b_along_n, sym;
     bool reduce;      // sum the previous phase's partial accumulators instead of a product
@@ -208,6 +210,9 @@ struct Tiling {
         return ratio * (tm * (tm - 1) / 2) + in_last;
     }
     static __host__ __device__ __forceinline__ int slabs(const Phase& p) { return p.tile_n / kSlab; }
+    static __host__ __device__ __forceinline__ int k_blocks(const Phase& p) {
+        return (p.k + kTileK - 1) / kTileK * p.terms;
+    }
     // A reduce phase deals out single slabs, a split product parts of K.
     static __host__ __device__ __forceinline__ int units(int m, int batch, const Phase& p) {
         return tiles(m, p) * batch * (p.reduce ? slabs(p) : p.splits);
@@ -237,7 +242,7 @@ struct Tiling {
             a.i = 8 * g + q % h;
             a.j = q / h;
         }
-        const int blocks = (p.k + kTileK - 1) / kTileK;
+        const int blocks = k_blocks(p);
         a.k0 = p.reduce ? 0 : blocks * part / p.splits;
         a.k1 = p.reduce ? 0 : blocks * (part + 1) / p.splits;
         a.slab0 = p.reduce ? part : 0;
@@ -365,7 +370,7 @@ __device__ __forceinline__ void finish_row(unsigned char* slab, int row, float (
             if constexpr (kResult == kState) {
                 unpack_half8(w, y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(__fsub_rn(x[i], y[i]), kLoScale);
+                for (int i = 0; i < 8; ++i) y[i] = __fsub_rn(x[i], y[i]);
                 *reinterpret_cast<uint4*>(slab + kPlaneBytes + swizzled(row, c0 + c)) = pack_half8(y);
             }
             if constexpr (kTranspose && kSources < 2) store_transposed(slab + kPlaneBytes, row, c0 + c, w);
@@ -453,8 +458,10 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
             if (p.reduce) continue;
             const int cols = p.tile_n / kPair;   // of B per CTA: 128 or 64
             const uint32_t bytes = kPair * (kOperandBytes + cols * kTileK * 2);
+            const CUtensorMap* maps_b = p.b_along_n || cols == 64 ? run.narrow : run.wide;
             const CUtensorMap* map_a = &run.wide[p.a];
-            const CUtensorMap* map_b = p.b_along_n || cols == 64 ? &run.narrow[p.b] : &run.wide[p.b];
+            const CUtensorMap* map_b = &maps_b[p.b];
+            const int term_blocks = T::k_blocks(p) / p.terms;
             const int units = T::units(run.m, run.batch, p);
             for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
                 const UnitAt at = T::at(run.m, p, u);
@@ -464,6 +471,13 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                 }
                 const int row = at.i * T::kTile + rank * kBlock, col = at.j * p.tile_n + rank * cols;
                 for (int kb = at.k0; kb < at.k1; ++kb) {
+                    int k = kb * kTileK;
+                    if (p.terms > 1) {
+                        const int term = kb / term_blocks;
+                        k -= term * term_blocks * kTileK;
+                        map_a = &run.wide[term == 1 ? p.a_lo : p.a];
+                        map_b = &maps_b[term == 2 ? p.b_lo : p.b];
+                    }
                     if (!__all_sync(kAll, mbar_wait(&empty[stage], phase ^ 1u))) {
                         late = true;
                         break;
@@ -473,13 +487,13 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                     const uint32_t bar = full0 + stage * 8;
                     if (issuer) {
                         if (rank == 0) mbar_expect_tx(&full[stage], bytes);
-                        tma_load<kPair>(a, map_a, kb * kTileK, row, at.b, bar);
+                        tma_load<kPair>(a, map_a, k, row, at.b, bar);
                         if (p.b_along_n) {
-                            tma_load<kPair>(b, map_b, col, kb * kTileK, at.b, bar);
+                            tma_load<kPair>(b, map_b, col, k, at.b, bar);
                             if (cols > 64)
-                                tma_load<kPair>(b + kOperandBytes / 2, map_b, col + 64, kb * kTileK, at.b, bar);
+                                tma_load<kPair>(b + kOperandBytes / 2, map_b, col + 64, k, at.b, bar);
                         } else {
-                            tma_load<kPair>(b, map_b, kb * kTileK, col, at.b, bar);
+                            tma_load<kPair>(b, map_b, k, col, at.b, bar);
                         }
                     }
                     __syncwarp();
@@ -754,7 +768,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                         const Count<1> one;
                         const Count<2> two;
                         const Result<kPlane> plane;
-                        if (p.result == kState) finish(two, Result<kState>(), No());
+                        if (p.result == kState) p.src2 == kNone ? finish(one, Result<kState>(), No()) : finish(two, Result<kState>(), No());
                         else if (p.result == kBf16) finish(two, Result<kBf16>(), No());
                         else if (p.result == kBf16Transposed) finish(two, Result<kBf16Transposed>(), No());
                         else if (p.src1 == kNone) mirror ? finish(none, plane, Yes()) : finish(none, plane, No());
@@ -809,7 +823,7 @@ k_orth_finish(const __half* __restrict__ hi, const __half* __restrict__ lo, int6
         const int64_t r = r0 + warp + 8 * i, c = c0 + lane;
         if (r >= m || c >= n || !SPL_CHECK(c < ld, kSiteOrthState, c)) continue;
         const int64_t at = b * plane + r * ld + c;
-        const float x = __fmul_rn(f, __fmaf_rn(__half2float(lo[at]), 1.0f / kLoScale, __half2float(hi[at])));
+        const float x = __fmul_rn(f, __fadd_rn(__half2float(hi[at]), __half2float(lo[at])));
         if (tall) s_tile[warp + 8 * i][lane] = x;
         else Vec16<true>::store1(out, (b * m + r) * n + c, x);
     }

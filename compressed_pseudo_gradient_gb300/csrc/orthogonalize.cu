@@ -14,10 +14,11 @@
 // values).  fp16's short range is met by fixed powers of two: X is held times x_scale =
 // 2^round(log2(n) / 2), which brings its entries near 1 (they are near n^-1/2), A and B times
 // 2^10 (diagonals near 1, off-diagonals down to 1e-6).  The state X itself keeps 22 bits, as
-// the sum of two fp16 planes hi + lo 2^-11: rounding X to 11 bits in every step would feed noise
+// the sum of two fp16 planes hi + lo: rounding X to 11 bits in every step would feed noise
 // of 2^-12 of the largest singular direction into the smallest ones, which the iteration then
 // amplifies (2e-2 of error on steep spectra; with the two planes 1e-3 to 1.7e-3 on all of them,
-// below the 1.7e-3 of the output's own rounding to bf16).  Only hi enters the products.
+// below the 1.7e-3 of the output's own rounding to bf16).  Only hi enters the products, but for
+// matrices of few rows (is_fine).
 //
 // orth_small.cuh has the kernel for matrices that fit a cluster, orth_run.cuh the one for all
 // others with orth_prep.cuh before it; this file chooses between them and lays out their work.
@@ -62,6 +63,13 @@ constexpr int kSplitBlocks = 4;  // of at least 4 blocks each
 // Whether a group of steps pays for a matrix of these sides (see group_steps).
 bool may_group(int64_t m, int64_t n) { return 4 * n >= 5 * m && m >= 256; }
 
+// Whether the phases' update of X also multiplies what the operands' rounding cuts off, B X as
+// B_hi X_hi + B_lo X_hi + B_hi X_lo: with few rows the roundings average out less (3.1e-3 of error
+// before the output's rounding at 32 rows, 1.6e-3 with the low planes; 1.8e-3 without at 64, 1.9e-3
+// at 128).  40 x 8000: 5 us of 126; a stack of 100 x (128 x 4096), bound by the operands' way from
+// L2, would take 1,084 us instead of 790.
+bool is_fine(int64_t m) { return m < kFineRows; }
+
 struct OrthLayout {
     int64_t m, n, ldx, ldm;   // short and long side, row pitches of X and of the square matrices
     size_t hi[2], lo[2], square[kSquares], arrived, partials, norms, bytes;
@@ -85,7 +93,7 @@ OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
         l.hi[i] = take(plane);
         l.lo[i] = take(plane);
     }
-    const int squares = may_group(l.m, l.n) ? kSquares : 2;
+    const int squares = may_group(l.m, l.n) ? kSquares : is_fine(l.m) ? 3 : 2;
     for (int i = 0; i < kSquares; ++i)
         l.square[i] = i < squares ? take(static_cast<size_t>(batch * l.m * l.ldm) * 2) : 0;
     l.arrived = take(kMaxPhases * kMaxSlots * 4);
@@ -177,6 +185,7 @@ struct PhaseList {
     int16_t last() const { return static_cast<int16_t>(num - 1); }
     void add(Phase ph) {
         ph.splits = 1;
+        if (ph.terms == 0) ph.terms = 1;
         ph.after[0] = last();
         ph.after[1] = -1;
         phases[num++] = ph;
@@ -229,7 +238,7 @@ double plan(const PhaseList& list, const OrthRun& run, int groups, size_t partia
     bool split = false, any_split = false;
     for (int i = 0; i < list.num; ++i) {
         Phase ph = list.phases[i];
-        const int blocks = (ph.k + kTileK - 1) / kTileK;
+        const int blocks = T::k_blocks(ph);
         auto time = [&](int tile_n, int splits) {
             Phase q = ph;
             q.tile_n = tile_n;
@@ -418,14 +427,15 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& a, bool bf16, cudaStre
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
         }
     };
-    enum : uint8_t { kHi0, kHi1, kLo0, kLo1, kOut, kSquare0 };
+    enum : uint8_t { kHi0, kHi1, kLo0, kLo1, kOut, kSquare0, kSquareLo = kSquare0 + 2 };
     const auto f16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     for (int i = 0; i < 2; ++i) {
         matrix(kHi0 + i, ws + l.hi[i], f16, l.m, l.n, l.ldx);
         matrix(kLo0 + i, ws + l.lo[i], f16, l.m, l.n, l.ldx);
     }
     const int grouped = group_steps(l.m, l.n, a.steps, a.coef[0]);
-    for (int i = 0; i < (grouped > 1 ? kSquares : 2); ++i)
+    const bool fine = is_fine(l.m);
+    for (int i = 0; i < (grouped > 1 ? kSquares : fine ? 3 : 2); ++i)
         matrix(kSquare0 + i, ws + l.square[i], f16, l.m, l.m, l.ldm);
     const bool direct = a.cols % 8 == 0;   // the output's rows are whole 16 bytes
     if (direct) matrix(kOut, a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.rows, a.cols, a.cols);
@@ -461,6 +471,10 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& a, bool bf16, cudaStre
                 const bool more = i + 1 < size;
                 const uint8_t B = take();   // B = b A + c A A
                 list.square(A, A, A, kNone, B, m, m, a.coef[2] / kGramScale, a.coef[1], 0.0f);
+                if (fine) {   // one tile, so without a mirror image: both its planes are kept
+                    list.phases[list.last()].result = kState;
+                    list.phases[list.last()].dst_lo = kSquareLo;
+                }
                 const int16_t poly = list.last();
                 uint8_t next = B;
                 int16_t rest = poly;
@@ -500,7 +514,12 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& a, bool bf16, cudaStre
             ph.k = m;
             ph.f_acc = out / kGramScale;
             ph.f1 = out * f;
-            ph.f2 = ph.f1 / kLoScale;
+            ph.f2 = ph.f1;
+            if (fine) {
+                ph.terms = 3;
+                ph.a_lo = kSquareLo;
+                ph.b_lo = lo;
+            }
             list.add(ph);
             give(R);
         }

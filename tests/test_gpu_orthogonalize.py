@@ -55,6 +55,19 @@ def test_matrix(m, n, dtype):
     assert off(got, iterate(u)) <= limit(m, n)
 
 
+@pytest.mark.parametrize("batch,m,n", [(1, 24, 5000), (1, 32, 9001), (2, 48, 6000), (1, 100, 5000), (1, 128, 8192),
+                                       (40, 48, 4096)])
+def test_few_long_rows(batch, m, n):
+    """Few rows average roundings less, and are multiplied in two planes: still 2e-3 before the output's
+    rounding, whose 1.7e-3 (2-norm, mantissas spread evenly) adds in quadrature."""
+    u = torch.randn(batch, m, n, generator=gen(m), device=DEV)
+    u *= torch.exp(math.log(100) * torch.rand(batch, m, 1, generator=gen(n), device=DEV))
+    for x in (u, u.mT.contiguous()):
+        got, ref = spl.orthogonalize(x), iterate(x)
+        for i in range(batch):
+            assert off(got[i], ref[i]) <= math.hypot(2e-3, 1.7e-3)
+
+
 @pytest.mark.parametrize("batch,m,n", [(12, 520, 1100), (3, 2100, 2300), (1, 2560, 3000)])
 @pytest.mark.parametrize("tall", [False, True])
 def test_many_tiles(batch, m, n, tall):
