@@ -273,8 +273,10 @@ double plan(const PhaseList& list, const OrthRun& run, int groups, size_t partia
                 }
         total += time(ph.tile_n, best);
         const int tiles = T::tiles(run.m, ph) * run.batch;
-        // the parts of two products beside each other would share the partials' memory
-        if (i > 0 && (best > 1 || split)) ph.after[0] = static_cast<int16_t>(i - 1), ph.after[1] = -1;
+        // the parts of two products beside each other would share the partials' memory; a product that
+        // waits for both of two beside each other goes on doing so
+        if (i > 0 && (best > 1 || split) && ph.after[0] != i - 1)
+            ph.after[0] = static_cast<int16_t>(i - 1), ph.after[1] = -1;
         split = best > 1;
         any_split |= split;
         const bool beside = ph.after[0] >= 0 && ph.after[0] != i - 1;
