@@ -11,11 +11,13 @@
 //   value = f_acc * accumulator + f1 * source1 + f2 * source2
 //
 // written as one fp16 plane (a symmetric product also to its mirrored place), as the state's two
-// planes, or as bf16 (in place or transposed).  Per CTA: one thread issues the operands' TMA loads
-// into a ring of stages, one the MMAs, one the TMA loads of the sources' 128 x 64 slabs, two sets
-// of four warps turn accumulators into results in the slabs' shared memory, a slab each, and one
-// thread issues the TMA stores that take them from there.  Two accumulators in tensor memory let a
-// tile's MMAs run under the previous tile's epilogue.
+// planes, or as bf16 (in place or transposed).  Per CTA: one warp issues the operands' TMA loads
+// into a ring of stages, one the MMAs, one thread the TMA loads of the sources' 128 x 64 slabs, two
+// sets of four warps turn accumulators into results in the slabs' shared memory, a slab each, and
+// one thread issues the TMA stores that take them from there.  Two accumulators in tensor memory let
+// a tile's MMAs run under the previous tile's epilogue.  The phase that sums a split product's parts
+// gets them by bulk copies into the then idle stages, four slabs ahead (with loads by the summing
+// threads 64 x 8000 takes 121 us instead of 114, 512 x 4096 153 instead of 147).
 //
 // Bound: large products by the tensor cores under the power limit (8192 x 8192 x 28672 at 1.6
 // PFLOP/s, against 1.74 sustained by a plain library product); those of matrices up to about 2,000
@@ -135,6 +137,12 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                      ::"r"(smem_addr(bar)) : "memory");
+}
+
+// A contiguous piece of global memory into shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
 
 // One lane of a converged warp.  The roles that issue operand copies and MMAs run with their whole
@@ -392,6 +400,13 @@ using Count = std::integral_constant<int, kCount>;
 template <ResultKind kResult>
 using Result = std::integral_constant<ResultKind, kResult>;
 
+// Where a slab of 64 columns of a unit's partial accumulators lies, in one piece.
+template <int kPair>
+__device__ __forceinline__ float4* partial_slab(const OrthRun& run, int unit, int rank, int slab) {
+    return reinterpret_cast<float4*>(run.partials) +
+           ((static_cast<int64_t>(unit) * kPair + rank) * (Tiling<kPair>::kTile / 4) + slab * (kSlab / 4)) * kBlock;
+}
+
 template <int kPair>
 __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_constant__ OrthRun run) {
     using T = Tiling<kPair>;
@@ -401,7 +416,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char* slabs = stages + kStages * kStageBytes;
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2],
-        src_full[kSlabs], src_empty[kSlabs], done[kSlabs], read[2], drain;
+        src_full[kSlabs], src_empty[kSlabs], done[kSlabs], read[2], part_full[kStages], part_empty[kStages], drain;
     __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = kPair == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
@@ -411,6 +426,8 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&part_full[s], 1);
+            mbar_init(&part_empty[s], 4);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&acc_full[s], 1);
@@ -576,7 +593,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
     } else if (warp == 10) {
         if (lane == 0) {   // sources
             Dependencies<kPair> deps;
-            int buf = 0, used = 0;
+            int buf = 0, used = 0, part = 0;
             uint32_t phase = 0;
             for (int ph = 0; ph < run.num_phases && !late; ++ph) {
                 const Phase p = run.phases[ph];
@@ -608,11 +625,27 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                             buf = 0;
                             phase ^= 1u;
                         }
+                        // This slab of each of the tile's partial accumulators, through the operands'
+                        // stages: the products before this phase are complete, those after it wait.
+                        for (int q = 0; q < (p.reduce ? p.splits : 0); ++q, ++part) {
+                            const int to = part % kStages;
+                            if (!mbar_wait(&part_empty[to], (part / kStages & 1) ^ 1u)) {
+                                late = true;
+                                break;
+                            }
+                            mbar_expect_tx(&part_full[to], kStageBytes);
+                            bulk_load(stages + to * kStageBytes,
+                                      partial_slab<kPair>(run, at.tile * p.splits + q, rank, s), kStageBytes,
+                                      &part_full[to]);
+                        }
+                        if (late) break;
                     }
                 }
             }
             if (late) {
                 bool pending = false;
+                for (int q = part > kStages ? part - kStages : 0; q < part; ++q)
+                    pending |= !mbar_wait(&part_full[q % kStages], q / kStages & 1);
                 for (int q = 0; q < used; ++q) {
                     const int s = (buf + kSlabs - 1 - q) % kSlabs;
                     pending |= !mbar_wait(&src_full[s], s < buf ? phase : phase ^ 1u);
@@ -677,10 +710,9 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
         }
         __syncwarp();
     } else {   // results
-        Dependencies<kPair> deps;
         // warps 0-3 take the even slabs in the order of the CTA's work, 4-7 the odd ones
         const int set = warp >> 2, quarter = warp & 3, row_in = quarter * 32 + lane;
-        int acc = 0, slab_count = 0;
+        int acc = 0, slab_count = 0, part = 0;   // part: of the partial accumulators summed
         uint32_t acc_phase = 0, read_phase = 0;
         for (int ph = 0; ph < run.num_phases && !late; ++ph) {
             const Phase p = run.phases[ph];
@@ -688,13 +720,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
             for (int u = (group + groups - p.first % groups) % groups; u < units && !late; u += groups) {
                 const UnitAt at = T::at(run.m, p, u);
                 const int row0 = at.i * T::kTile + rank * kBlock;
-                if (p.reduce) {
-                    const bool ok = deps.wait(run, p, ph, at.b);
-                    if (__any_sync(kAll, !ok)) {
-                        late = true;
-                        break;
-                    }
-                } else {
+                if (!p.reduce) {
                     const bool ok = mbar_wait(&acc_full[acc], acc_phase);
                     if (__any_sync(kAll, !ok)) {
                         late = true;
@@ -707,7 +733,10 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                     if (col0 >= p.n) break;
                     const int buf = slab_count % kSlabs;
                     const uint32_t phase = slab_count / kSlabs & 1;
-                    if ((slab_count++ & 1) != set) continue;
+                    if ((slab_count++ & 1) != set) {
+                        if (p.reduce) part += p.splits;
+                        continue;
+                    }
                     float v[kSlab];
                     if (!p.reduce) {
                         const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -722,33 +751,36 @@ __global__ void __launch_bounds__(kRunThreads, 1) k_orth_run(const __grid_consta
                         break;
                     }
                     unsigned char* slab = slabs + buf * kSlabBytes;
-                    // where this thread's row of a unit's partial accumulators starts
-                    auto partial = [&](int unit) {
-                        return reinterpret_cast<float4*>(run.partials) +
-                               ((static_cast<int64_t>(unit) * kPair + rank) * (T::kTile / 4) +
-                                s * (kSlab / 4)) * kBlock + row_in;
-                    };
                     if (p.result == kPartial) {
-                        float4* to = partial(u);
+                        float4* to = partial_slab<kPair>(run, u, rank, s) + row_in;
 #pragma unroll
                         for (int c = 0; c < kSlab / 4; ++c)
                             to[c * kBlock] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
                         __threadfence();
+                        fence_async_global();   // read by bulk copies
                     } else {
                         if (p.reduce) {
 #pragma unroll
                             for (int c = 0; c < kSlab; ++c) v[c] = 0.0f;
-                            for (int q = 0; q < p.splits; ++q) {   // in the order of K
-                                const float4* from = partial(at.tile * p.splits + q);
+                            for (int q = 0; q < p.splits && !late; ++q, ++part) {   // in the order of K
+                                const int from = part % kStages;
+                                if (__any_sync(kAll, !mbar_wait(&part_full[from], part / kStages & 1))) {
+                                    late = true;
+                                    break;
+                                }
+                                const float4* x = reinterpret_cast<const float4*>(stages + from * kStageBytes) + row_in;
 #pragma unroll
                                 for (int c = 0; c < kSlab / 4; ++c) {
-                                    const float4 x = __ldcg(from + c * kBlock);
-                                    v[4 * c] = __fadd_rn(v[4 * c], x.x);
-                                    v[4 * c + 1] = __fadd_rn(v[4 * c + 1], x.y);
-                                    v[4 * c + 2] = __fadd_rn(v[4 * c + 2], x.z);
-                                    v[4 * c + 3] = __fadd_rn(v[4 * c + 3], x.w);
+                                    const float4 y = x[c * kBlock];
+                                    v[4 * c] = __fadd_rn(v[4 * c], y.x);
+                                    v[4 * c + 1] = __fadd_rn(v[4 * c + 1], y.y);
+                                    v[4 * c + 2] = __fadd_rn(v[4 * c + 2], y.z);
+                                    v[4 * c + 3] = __fadd_rn(v[4 * c + 3], y.w);
                                 }
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&part_empty[from]);
                             }
+                            if (late) break;
                         }
                         const bool mirror = p.sym && !T::on_diagonal(p, at.i, at.j);
                         // the four warps of the set have read this slab's sources

@@ -66,7 +66,7 @@ bool may_group(int64_t m, int64_t n) { return 4 * n >= 5 * m && m >= 256; }
 // Whether the phases' update of X also multiplies what the operands' rounding cuts off, B X as
 // B_hi X_hi + B_lo X_hi + B_hi X_lo: with few rows the roundings average out less (3.1e-3 of error
 // before the output's rounding at 32 rows, 1.6e-3 with the low planes; 1.8e-3 without at 64, 1.9e-3
-// at 128).  40 x 8000: 5 us of 126; a stack of 100 x (128 x 4096), bound by the operands' way from
+// at 128).  40 x 8000: 5 us of about 120; a stack of 100 x (128 x 4096), bound by the operands' way from
 // L2, would take 1,084 us instead of 790.
 bool is_fine(int64_t m) { return m < kFineRows; }
 
