@@ -80,8 +80,10 @@ OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
     OrthLayout l;
     l.m = rows <= cols ? rows : cols;
     l.n = rows <= cols ? cols : rows;
-    l.ldx = (l.n + 7) / 8 * 8;   // TMA wants row pitches of whole 16 bytes
-    l.ldm = (l.m + 7) / 8 * 8;
+    // Rows of whole 128 bytes: TMA would take pitches of 16, but a box's rows of 128 bytes then lie
+    // over two lines of L2 each (12 x 500 x 1000: 188 us instead of 167, 3000 x 5000: 1,063 and 854)
+    l.ldx = (l.n + 63) / 64 * 64;
+    l.ldm = (l.m + 63) / 64 * 64;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
